@@ -354,8 +354,9 @@ const char* qsa_last_error(void);
  * second): that launch left its output incomplete and returned early instead
  * of hanging the GPU.  Bit 1: a top-k launch gave up waiting for its row copy
  * (its selection for that row is unspecified).  Bit 2: a qsa_page_stream
- * launch gave up waiting for a page (its checksum is unspecified).  Synchronises the current
- * device, then writes the word to *flags (host pointer).  When `clear` is
+ * launch gave up waiting for a page (its checksum is unspecified).  Bit 3: a
+ * qsa_paged_attention launch gave up waiting for a copy or a product (its
+ * output is unspecified).  Synchronises the current device, then writes the word to *flags (host pointer).  When `clear` is
  * non-zero it then clears the word and zeroes the counter array of
  * qsa_paged_mqa_topk_noalloc on the current device (synchronously), so the
  * next no-alloc call starts clean after a failed one.
@@ -389,6 +390,223 @@ qsa_status qsa_device_status(uint32_t* flags, int32_t clear);
  */
 qsa_status qsa_page_stream(const void* base, int64_t page_stride, int32_t page_bytes, const int32_t* pages,
                            int64_t num_listed, int64_t pool_pages, uint32_t* checksum, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Serving operators around the indexer: what a step needs next to scoring and
+ * selection.  In the order in which a step runs them:
+ *
+ *   qsa_build_page_maps    block tables, slots, positions and visible counts of
+ *                          the step's tokens, from the requests' lengths;
+ *   qsa_store_paged_kv     the new tokens' keys and values into the paged cache;
+ *   qsa_store_index_keys   the new compressed keys into the paged index cache
+ *                          that qsa_paged_mqa_logits reads;
+ *   (scoring and top-k)
+ *   qsa_paged_attention    attention of the new tokens over the paged cache, or
+ *                          over the columns the top-k selected.
+ *
+ * The conventions above hold, with two differences.  These calls read nothing
+ * before the kernel ahead of them in the stream has completed (metadata
+ * included).  And qsa_build_page_maps writes block_table and visible_cols,
+ * which scoring and selection read early: another kernel (the stores, in a
+ * step) must stand between it and such a call in the stream.
+ * ------------------------------------------------------------------------- */
+
+/* 16-bit element types of keys, values, queries and outputs. */
+typedef enum qsa_half_dtype { QSA_HALF_BF16 = 0, QSA_HALF_F16 = 1 } qsa_half_dtype;
+
+/* Shape of one qsa_build_page_maps call (host values). */
+typedef struct qsa_page_maps_desc {
+  int32_t num_requests; /* B, 0..16384                                              */
+  int32_t page_tokens;  /* tokens a page holds, P >= 1                              */
+  int32_t max_pages;    /* entries of a block-table row that may be used, >= 1;
+                           max_pages * page_tokens < 2^31                           */
+  int32_t ratio;        /* tokens a compressed column covers, >= 1, divides P       */
+  int32_t partial_cols; /* visible counts: 0 complete columns, floor((p+1)/ratio);
+                           1 begun columns, ceil((p+1)/ratio)                       */
+  int32_t reserved;     /* 0                                                        */
+  int64_t table_stride; /* entries from one block-table row to the next, >= max_pages */
+  int64_t num_free;     /* entries of free_pages, >= 0                              */
+  int64_t max_tokens;   /* rows of the per-token outputs, 0..2^31-1                 */
+} qsa_page_maps_desc;
+
+/*
+ * qsa_build_page_maps - a step's page bookkeeping on the device.
+ *
+ * Request b holds c = max(context_lens[b], 0) tokens and gets n =
+ * max(new_lens[b], 0) more.  With have = ceil(c / P) and need = ceil((c+n) / P)
+ * (both at most max_pages), and first the sum of need - have over the requests
+ * before b:
+ *   block_table[b][j] = free_pages[first + j - have]   for have <= j < need
+ *                       (-1 where first + j - have >= num_free: list exhausted);
+ *   query_start[b]    = sum of n over the requests before b (query_start[B]: all);
+ *   seq_lens[b]       = c + n;
+ *   pages_used[0]     = sum of need - have (above num_free: that many were wanted).
+ * Token t, query_start[b] <= t < query_start[b+1], of request b, lies at
+ * position p = c + t - query_start[b]:
+ *   slots[t]          = block_table[b][p / P] * P + p % P, -1 when that page is
+ *                       missing (a negative entry, or p / P >= max_pages);
+ *   positions[t] = p; token_request[t] = b;
+ *   visible_cols[t]   = the columns the token sees (partial_cols);
+ *   column_slots[t]   = slots[t] / ratio when the token completes its column
+ *                       (p % ratio == ratio - 1) and has a slot, else -1.
+ * Rows t in [query_start[B], max_tokens) are padding: -1, -1, -1, 0, -1.
+ * Tokens past max_tokens are not written; query_start still counts them.
+ * The sums saturate at 2^31-1.
+ *
+ * Device pointers: context_lens, new_lens int32 [B]; free_pages int32
+ * [num_free]; block_table int32, updated in place; query_start int32 [B+1],
+ * seq_lens int32 [B], slots and column_slots int64 [max_tokens] (8-byte
+ * aligned), positions, token_request, visible_cols int32 [max_tokens],
+ * pages_used int32 [1].  query_start, seq_lens and slots may not be NULL;
+ * the other outputs may (not written).  No output may overlap an input.
+ * Calling again with the same lengths and free list writes the same values.
+ */
+qsa_status qsa_build_page_maps(const qsa_page_maps_desc* desc, const int32_t* context_lens,
+                               const int32_t* new_lens, const int32_t* free_pages, int32_t* block_table,
+                               int32_t* query_start, int32_t* seq_lens, int64_t* slots, int32_t* positions,
+                               int32_t* token_request, int32_t* visible_cols, int64_t* column_slots,
+                               int32_t* pages_used, void* stream);
+
+/* A paged key/value cache.  The key of (page p, slot j, head h) starts at
+ * (char*)k_cache + p*k_page_stride + j*k_token_stride + h*k_head_stride, its
+ * head_dim elements are contiguous; values alike.  All strides are bytes,
+ * positive multiples of 16; both bases are 16-byte aligned. */
+typedef struct qsa_kv_desc {
+  int32_t dtype;        /* qsa_half_dtype                              */
+  int32_t num_pages;    /* >= 1                                        */
+  int32_t page_tokens;  /* >= 1; num_pages * page_tokens < 2^62        */
+  int32_t num_kv_heads; /* >= 1                                        */
+  int32_t head_dim;     /* store: a multiple of 8, 8..1024; attention: 64 or 128 */
+  int32_t reserved;     /* 0                                           */
+  int64_t k_page_stride, k_token_stride, k_head_stride;
+  int64_t v_page_stride, v_token_stride, v_head_stride;
+} qsa_kv_desc;
+
+/*
+ * qsa_store_paged_kv - writes rows of keys and values into their cache slots.
+ *
+ * For t < num_tokens with 0 <= slots[t] < num_pages * page_tokens, and each
+ * head h: the head_dim elements at (char*)k + t*k_row_stride + h*k_row_head_stride
+ * go to the key of (slots[t] / page_tokens, slots[t] % page_tokens, h), and v's
+ * likewise.  Other rows are skipped.  Two rows with one slot: either may win.
+ * Row and head strides are bytes, multiples of 16; k and v 16-byte aligned;
+ * slots int64, 8-byte aligned.  num_tokens 0 launches nothing.
+ */
+qsa_status qsa_store_paged_kv(const qsa_kv_desc* desc, const void* k, int64_t k_row_stride,
+                              int64_t k_row_head_stride, const void* v, int64_t v_row_stride,
+                              int64_t v_row_head_stride, const int64_t* slots, int64_t num_tokens, void* k_cache,
+                              void* v_cache, void* stream);
+
+/* The paged index cache qsa_paged_mqa_logits reads (fields as in qsa_paged_desc). */
+typedef struct qsa_index_cache_desc {
+  int32_t kv_dtype;          /* qsa_kv_dtype                                     */
+  int32_t num_pages;         /* >= 1                                             */
+  int32_t page_cols;         /* >= 1                                             */
+  int32_t head_dim;          /* must be 128                                      */
+  int64_t key_page_stride;   /* bytes; bf16: a multiple of 16; fp8: of 4         */
+  int64_t scale_page_stride; /* bytes; fp8: a multiple of 4; bf16: 0             */
+} qsa_index_cache_desc;
+
+/*
+ * qsa_store_index_keys - writes compressed index keys into their cache slots.
+ *
+ * keys: bf16 rows of 128, row t at (char*)keys + t*row_stride (16-byte aligned,
+ * a multiple of 16); slots int64 [num_tokens], column slots as
+ * qsa_build_page_maps makes them; a row whose slot is outside
+ * [0, num_pages * page_cols) is skipped.
+ * bf16 cache: the row is copied.  fp8 cache: scale = max|x| / 448 (fp32,
+ * rounded to nearest), code = e4m3(x / scale) (the fp32 quotient, clamped to
+ * +-448, to the nearest code, ties to even; codes 0 when scale is 0); codes go
+ * to the key, the scale to (char*)scales + page*scale_page_stride + 4*slot.
+ * Keys are finite.  scales: NULL for bf16 (mixed operand types otherwise).
+ */
+qsa_status qsa_store_index_keys(const qsa_index_cache_desc* desc, const void* keys, int64_t row_stride,
+                                const int64_t* slots, int64_t num_tokens, void* kv_cache, float* scales,
+                                void* stream);
+
+/* Kernel forms of qsa_paged_attention (qsa_attn_desc.form, qsa_plan_attention). */
+typedef enum qsa_attn_form {
+  QSA_ATTN_AUTO = 0,
+  QSA_ATTN_GATHER = 1, /* key rows gathered one by one, warps on their own keys:
+                          few query rows a request, selected columns, any page size */
+  QSA_ATTN_TILE = 2    /* tcgen05 tiles of 128 query rows x 128 keys: chunks */
+} qsa_attn_form;
+
+/* Leading bytes of a qsa_paged_attention workspace that must start as zero. */
+#define QSA_ATTN_COUNTER_BYTES 640
+
+/* Shape of one qsa_paged_attention call (host values). */
+typedef struct qsa_attn_desc {
+  qsa_kv_desc kv;
+  int32_t num_requests;   /* B >= 0                                                   */
+  int32_t num_q_heads;    /* a multiple of num_kv_heads; query head h reads key/value
+                             head h / (num_q_heads / num_kv_heads); at most 256 to one */
+  int32_t max_pages;      /* entries of a block-table row, >= 1                       */
+  int32_t max_new;        /* the caller's bound on the new tokens of a request, or 0
+                             (unknown): chooses the form only, a wrong bound costs
+                             speed, never correctness                                 */
+  int32_t num_selected;   /* columns listed per token row (k), 0: every key is seen   */
+  int32_t ratio;          /* tokens a selected column covers, >= 1                    */
+  int32_t local_tokens;   /* with num_selected > 0: the last tokens every row sees, >= 0 */
+  int32_t form;           /* qsa_attn_form                                            */
+  int64_t num_tokens;     /* rows of q and out, 0..2^31-1                             */
+  int64_t table_stride;   /* entries from one block-table row to the next             */
+  int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride; /* bytes,
+                             positive multiples of 16                                 */
+  float scale;            /* finite, > 0                                              */
+  int32_t reserved;       /* 0                                                        */
+} qsa_attn_desc;
+
+/*
+ * qsa_paged_attention - attention of each request's new tokens over its cache.
+ *
+ * Request b's new tokens are rows query_start[b] <= t < query_start[b+1] of q,
+ * the last ones of its seq_lens[b] tokens: with n rows, row i lies at position
+ * p = seq_lens[b] - n + i.  Their own keys and values are in the cache already.
+ * Row t sees the tokens j (0 <= j <= p, j < max_pages * page_tokens) and, when
+ * num_selected > 0, of these only
+ *   - the tokens c*ratio .. c*ratio + ratio-1 of the columns c >= 0 listed in
+ *     selected[t][0..num_selected) that lie before p + 1 - local_tokens, and
+ *   - the last local_tokens tokens, j >= p + 1 - local_tokens.
+ * Entries below 0 list nothing (as qsa_select_topk pads); a column may be
+ * listed at most once.  With x_j = scale * dot(q[t][h], K_j):
+ *   out[t][h] = sum_j exp(x_j - lse) V_j,   lse[t][h] = log(sum_j exp(x_j)),
+ * accumulated in fp32 (the probabilities enter the second product in the
+ * 16-bit type); a row that sees nothing gets zeros and -inf.
+ * Rows t >= query_start[B] are not written.  Cache contents past seq_lens[b],
+ * and pages no listed entry names, are never used, whatever they hold (NaN
+ * included); the visible tokens' keys and values are finite.
+ *
+ * Device pointers: q and out in the cache's 16-bit type, 16-byte aligned;
+ * block_table int32; query_start int32 [B+1], non-decreasing, clamped to
+ * [0, num_tokens]; seq_lens int32 [B]; selected int32 [num_tokens][num_selected]
+ * or NULL when num_selected is 0; lse fp32 [num_tokens][num_q_heads] or NULL.
+ * Page ids are clamped to [0, num_pages).
+ * workspace: device memory of at least qsa_paged_attention_workspace(desc)
+ * bytes, 16-byte aligned, whose first QSA_ATTN_COUNTER_BYTES are zero before
+ * its first use; every completed call leaves them zero again, whatever its
+ * shape and form (a call that set qsa_device_status bit 3 may not: zero them
+ * then).  Calls that may run at the
+ * same time need workspaces of their own.  The results do not depend on what
+ * runs beside the call: splits of the keys are joined in a fixed order.
+ *
+ * QSA_ERR_UNSUPPORTED: head_dim other than 64 and 128, a forced form that does
+ * not serve the shape.
+ */
+qsa_status qsa_paged_attention(const qsa_attn_desc* desc, const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_table, const int32_t* query_start, const int32_t* seq_lens,
+                               const int32_t* selected, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of a qsa_paged_attention call (host only): the unfinished
+ * parts of the key splits, two a CTA, so independent of the lengths. */
+qsa_status qsa_paged_attention_workspace(const qsa_attn_desc* desc, size_t* bytes);
+
+/* The form qsa_paged_attention takes for `desc` (host only): tiles when a
+ * request may bring more than 32 query rows a key/value head, no columns are
+ * selected and pages hold 8, 16, 32, 64 or a multiple of 128 tokens; else
+ * gathered rows. */
+qsa_status qsa_plan_attention(const qsa_attn_desc* desc, int32_t* form);
 
 /* QSA_ABI_VERSION of the loaded library. */
 int32_t qsa_abi_version(void);

@@ -27,7 +27,12 @@ EXPORTED = ("qsa_paged_mqa_logits", "qsa_paged_mqa_logits_ragged", "qsa_paged_mq
             "qsa_paged_mqa_topk_noalloc_counters", "qsa_select_topk", "qsa_select_topk_bounded", "qsa_plan_variant",
             "qsa_plan_variant_ex", "qsa_force_variant",
             "qsa_last_variant", "qsa_status_string", "qsa_last_error", "qsa_abi_version", "qsa_device_status",
-            "qsa_page_stream")
+            "qsa_page_stream", "qsa_build_page_maps", "qsa_store_paged_kv", "qsa_store_index_keys",
+            "qsa_paged_attention", "qsa_paged_attention_workspace", "qsa_plan_attention")
+
+HALF_BF16, HALF_F16 = 0, 1
+ATTN_AUTO, ATTN_GATHER, ATTN_TILE = 0, 1, 2
+ATTN_COUNTER_BYTES = 640
 
 
 class QSAError(RuntimeError):
@@ -50,6 +55,33 @@ class PagedDesc(ctypes.Structure):
         ("key_page_stride", ctypes.c_int64),
         ("scale_page_stride", ctypes.c_int64),
     ]
+
+
+class PageMapsDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_requests", "page_tokens", "max_pages", "ratio", "partial_cols",
+                                              "reserved")] + \
+               [(n, ctypes.c_int64) for n in ("table_stride", "num_free", "max_tokens")]
+
+
+class KvDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "num_pages", "page_tokens", "num_kv_heads", "head_dim",
+                                              "reserved")] + \
+               [(n, ctypes.c_int64) for n in ("k_page_stride", "k_token_stride", "k_head_stride", "v_page_stride",
+                                              "v_token_stride", "v_head_stride")]
+
+
+class IndexCacheDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("kv_dtype", "num_pages", "page_cols", "head_dim")] + \
+               [(n, ctypes.c_int64) for n in ("key_page_stride", "scale_page_stride")]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [("kv", KvDesc)] + \
+               [(n, ctypes.c_int32) for n in ("num_requests", "num_q_heads", "max_pages", "max_new", "num_selected",
+                                              "ratio", "local_tokens", "form")] + \
+               [(n, ctypes.c_int64) for n in ("num_tokens", "table_stride", "q_token_stride", "q_head_stride",
+                                              "out_token_stride", "out_head_stride")] + \
+               [("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -102,6 +134,19 @@ def load_library():
         lib.qsa_page_stream.restype = ctypes.c_int
         lib.qsa_page_stream.argtypes = [ctypes.c_void_p, ctypes.c_int64, i32, ctypes.c_void_p, ctypes.c_int64,
                                         ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]
+        sz, ptr = ctypes.c_size_t, ctypes.POINTER
+        lib.qsa_build_page_maps.restype = ctypes.c_int
+        lib.qsa_build_page_maps.argtypes = [ptr(PageMapsDesc)] + [vp] * 13
+        lib.qsa_store_paged_kv.restype = ctypes.c_int
+        lib.qsa_store_paged_kv.argtypes = [ptr(KvDesc), vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, vp]
+        lib.qsa_store_index_keys.restype = ctypes.c_int
+        lib.qsa_store_index_keys.argtypes = [ptr(IndexCacheDesc), vp, i64, vp, i64, vp, vp, vp]
+        lib.qsa_paged_attention.restype = ctypes.c_int
+        lib.qsa_paged_attention.argtypes = [ptr(AttnDesc)] + [vp] * 10 + [sz, vp]
+        lib.qsa_paged_attention_workspace.restype = ctypes.c_int
+        lib.qsa_paged_attention_workspace.argtypes = [ptr(AttnDesc), ptr(sz)]
+        lib.qsa_plan_attention.restype = ctypes.c_int
+        lib.qsa_plan_attention.argtypes = [ptr(AttnDesc), ptr(i32)]
         _lib = lib
     return _lib
 
@@ -248,3 +293,48 @@ def device_status(clear: bool = True) -> int:
 
 def abi_version() -> int:
     return load_library().qsa_abi_version()
+
+
+def build_page_maps(desc: PageMapsDesc, context_lens, new_lens, free_pages, block_table, query_start, seq_lens, slots,
+                    positions=None, token_request=None, visible_cols=None, column_slots=None, pages_used=None,
+                    stream=None) -> None:
+    _check(load_library().qsa_build_page_maps(
+        ctypes.byref(desc), _addr(context_lens), _addr(new_lens), _addr(free_pages), _addr(block_table),
+        _addr(query_start), _addr(seq_lens), _addr(slots), _addr(positions), _addr(token_request),
+        _addr(visible_cols), _addr(column_slots), _addr(pages_used), _stream(stream)))
+
+
+def store_paged_kv(desc: KvDesc, k, k_row_stride: int, k_row_head_stride: int, v, v_row_stride: int,
+                   v_row_head_stride: int, slots, num_tokens: int, k_cache, v_cache, stream=None) -> None:
+    _check(load_library().qsa_store_paged_kv(
+        ctypes.byref(desc), _addr(k), int(k_row_stride), int(k_row_head_stride), _addr(v), int(v_row_stride),
+        int(v_row_head_stride), _addr(slots), int(num_tokens), _addr(k_cache), _addr(v_cache), _stream(stream)))
+
+
+def store_index_keys(desc: IndexCacheDesc, keys, row_stride: int, slots, num_tokens: int, kv_cache, scales,
+                     stream=None) -> None:
+    _check(load_library().qsa_store_index_keys(ctypes.byref(desc), _addr(keys), int(row_stride), _addr(slots),
+                                               int(num_tokens), _addr(kv_cache), _addr(scales), _stream(stream)))
+
+
+def paged_attention(desc: AttnDesc, q, k_cache, v_cache, block_table, query_start, seq_lens, selected, out, lse,
+                    workspace, workspace_bytes: int, stream=None) -> None:
+    _check(load_library().qsa_paged_attention(
+        ctypes.byref(desc), _addr(q), _addr(k_cache), _addr(v_cache), _addr(block_table), _addr(query_start),
+        _addr(seq_lens), _addr(selected), _addr(out), _addr(lse), _addr(workspace), int(workspace_bytes),
+        _stream(stream)))
+
+
+def paged_attention_workspace_bytes(desc: AttnDesc) -> int:
+    """Workspace bytes paged_attention needs for this shape (its first
+    ATTN_COUNTER_BYTES zeroed before first use)."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().qsa_paged_attention_workspace(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def plan_attention(desc: AttnDesc) -> int:
+    """The form (ATTN_GATHER or ATTN_TILE) paged_attention takes for this shape."""
+    v = ctypes.c_int32(0)
+    _check(load_library().qsa_plan_attention(ctypes.byref(desc), ctypes.byref(v)))
+    return v.value

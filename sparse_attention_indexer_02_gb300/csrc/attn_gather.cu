@@ -1,0 +1,554 @@
+// qsa_paged_attention, gathered form: few query rows a request, or rows that
+// each see their own selected columns.
+//
+// One pass over the keys with a running maximum and sum.  For row i with
+// scores x_j = scale * q_i . k_j (kept in units of log2): m = max x_j,
+// l = sum 2^(x_j - m), o = sum 2^(x_j - m) v_j; when m grows, l and o are
+// multiplied by 2^(m_old - m_new).  Two such triples (m, l, o) over disjoint
+// keys join the same way, so keys can be split freely: over the warps of a CTA
+// and over CTAs.
+//
+// What bounds it is the key/value bytes: HBM for a decode step, whose 16 or 32
+// query rows do at most 32 flop a byte, L2 for chunks of selected rows.  So
+// the kernel is a stream first: every warp works alone on 16 keys at a time
+// (warp w of the CTA's 8 on keys 16 w .. 16 w + 15 of each 128-key unit) with
+// a ring of kStages 16-key stages of its own, and no barrier stands between
+// the warps until an item ends.  A stage is filled by 32 bulk copies, one a
+// lane: lanes 0-15 a key row each, lanes 16-31 a value row each.  Rows may lie
+// anywhere, so pages of any size, any cache strides and selected columns are
+// one path, and only rows that are seen are copied; the others are zeroed, so
+// that nothing a cache holds elsewhere can enter a product.  Rows are 16 bytes
+// apart more than their length, which keeps the matrix loads free of bank
+// conflicts.  192 KB of copies in flight on each SM cover the latency.
+//
+// The products are mma.sync (m16n8k16): with at most 32 query rows a tcgen05
+// tile of 128 rows would be three quarters padding, and the stream leaves the
+// tensor cores idle most of the time either way.  The probabilities go from
+// the accumulator layout of the first product straight into the operand layout
+// of the second, in registers, rounded to the 16-bit type there (relative
+// 2^-9 or 2^-12 a term; their sum is taken from the fp32 values).
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "attn_common.cuh"
+
+namespace qsa {
+namespace attn {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kNT = 32 * kWarps;
+constexpr int kStages = 3;
+constexpr int kSlice = kUnit / kWarps;  // keys a stage
+static_assert(kSlice == 16, "a stage is one k-step of the second product");
+
+template <int D>
+struct Geo {
+  static constexpr int kRow = 2 * D + 16;                  // bytes from row to row
+  static constexpr int kStage = 2 * kSlice * kRow;         // key rows, then value rows
+  static constexpr int kWarpBytes = kStages * kStage;
+  static constexpr int kMergeRow = D + 4;                  // floats from row to row of a warp's o
+};
+
+template <int D, int MT>
+struct Layout {
+  static constexpr int kRows = 16 * MT;
+  static constexpr int q = kWarps * Geo<D>::kWarpBytes;
+  static constexpr int ml = q + kRows * Geo<D>::kRow;          // [warp][row] of (m, l)
+  static constexpr int bars = ml + kWarps * kRows * 8;         // [warp][stage]
+  static constexpr int masks = bars + kWarps * kStages * 8;    // [warp][stage]
+  static constexpr int total = masks + kWarps * kStages * 4;
+  static_assert(kRows * Geo<D>::kMergeRow * 4 <= Geo<D>::kWarpBytes, "a warp's o fits its stages");
+  static_assert(total <= 226 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void bulk_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// An unfinished part: o [kRows][D] floats, then (m, l) of each row.
+template <int D, int MT>
+constexpr int64_t part_floats() {
+  return 16 * MT * (D + 2);
+}
+
+template <bool F16, int D, int MT, bool SEL>
+__global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p) {
+  using G = Geo<D>;
+  using L = Layout<D, MT>;
+  constexpr int kRows = 16 * MT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ SchedShared sched_sh;
+  __shared__ int abort_sh;
+  __shared__ int last_sh;
+  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::bars) + warp * kStages;
+  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + L::masks) + warp * kStages;
+  float2* ml = reinterpret_cast<float2*>(smem + L::ml);
+  uint8_t* ring = smem + warp * G::kWarpBytes;
+  const uint32_t ring_u32 = ptx::smem_u32(ring);
+  volatile int* abort_flag = &abort_sh;
+
+  if (lane == 0)
+    for (int s = 0; s < kStages; ++s) ptx::mbar_init(&bars[s], 1);
+  if (tid == 0) abort_sh = 0;
+  ptx::fence_mbar_init();
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+
+  // ---- the CTA's share of the units
+  const int32_t list_len = SEL ? p.num_selected * p.ratio + p.local_tokens : 0;
+  const int32_t sel_units = SEL ? units_of(list_len) : 0;
+  Schedule s;
+  int32_t sel_b = 0;
+  if (SEL) {
+    const int64_t rows = min(max(p.query_start[p.num_requests], 0), p.num_tokens);
+    s.total = rows * p.hv * sel_units;
+    const int64_t want = (s.total + p.min_units - 1) / p.min_units;
+    s.ge = (int)min((int64_t)gridDim.x, max((int64_t)1, want));
+    const int c = (int)blockIdx.x;
+    s.u0 = c < s.ge ? s.share(c) : s.total;
+    s.u1 = c < s.ge ? s.share(c + 1) : s.total;
+    __syncthreads();
+  } else {
+    s = make_schedule<kNT>(p, sched_sh);
+  }
+  if (s.u0 >= s.u1) return;
+
+  uint32_t issued = 0, used = 0;  // stages filled and consumed by this warp
+  bool ok = true;
+  const int r16 = lane & 15;
+  const bool is_v = lane >= 16;
+  const uint8_t* cache = is_v ? p.v : p.k;
+  const int64_t page_stride = is_v ? p.v_page_stride : p.k_page_stride;
+  const int64_t token_stride = is_v ? p.v_token_stride : p.k_token_stride;
+  const int64_t head_stride = is_v ? p.v_head_stride : p.k_head_stride;
+
+  Item it;
+  auto sel_item = [&](int64_t u) {  // SEL: the item of unit u (one token row, one head)
+    const int64_t i = u / sel_units;
+    const int32_t t = (int32_t)(i / p.hv);
+    it.hv = (int32_t)(i - (int64_t)t * p.hv);
+    it.s0 = i * sel_units;
+    it.s1 = it.s0 + sel_units;
+    it.row0 = t;
+    it.n = 1;
+    int lo = sel_b, hi = p.num_requests;  // the last request that starts at or before t
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.query_start[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    sel_b = it.b = lo;
+    const Request r = request_of(p, lo);
+    it.pos0 = r.pos0 + (t - r.first);
+    if (t >= r.first + r.n) it.pos0 = -1;
+    it.keys = min(max(it.pos0 + 1, 0), p.capacity);
+  };
+  Walker* walk = nullptr;
+  alignas(Walker) unsigned char walk_mem[sizeof(Walker)];
+  if (SEL) {
+    sel_item(s.u0);
+  } else {
+    walk = new (walk_mem) Walker(p, sched_sh, s.u0);
+    it = walk->it;
+  }
+
+  for (;;) {
+    const int64_t a = max(s.u0, it.s0), z = min(s.u1, it.s1);
+    const int ua = (int)(a - it.s0), uz = (int)(z - it.s0);
+    const int kvh = it.hv / p.splits;
+    const int sub0 = (it.hv - kvh * p.splits) * p.sub;
+    const int gs = min(p.sub, p.group - sub0);  // query heads of this virtual head
+    const int live = it.n * gs;
+    const int head0 = kvh * p.group + sub0;
+
+    // ---- q: rows (token, head) into shared memory, the padding rows zero
+    for (int i = tid; i < kRows * (D / 8); i += kNT) {
+      const int r = i / (D / 8), c = i - r * (D / 8);
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (r < live) {
+        const int tk = r / gs, g = r - tk * gs;
+        w = *reinterpret_cast<const uint4*>(p.q + (int64_t)(it.row0 + tk) * p.q_token_stride +
+                                            (int64_t)(head0 + g) * p.q_head_stride + c * 16);
+      }
+      *reinterpret_cast<uint4*>(smem + L::q + r * G::kRow + c * 16) = w;
+    }
+
+    // ---- key list: the token at place j * 128 + warp * 16 + r16 of unit j
+    const uint8_t* base = cache + (int64_t)kvh * head_stride;
+    const int32_t* table = p.block_table + (int64_t)it.b * p.table_stride;
+    const int32_t* sel = SEL ? p.selected + (int64_t)it.row0 * p.num_selected : nullptr;
+    const int32_t sel_end = SEL ? p.num_selected * p.ratio : 0;
+    const int32_t local0 = SEL ? it.pos0 + 1 - p.local_tokens : 0;  // first of the last tokens
+    auto sel_entry = [&](int j) -> int32_t {  // SEL: the column listed for the lane's place, -1 none
+      const int32_t at = j * kUnit + warp * kSlice + r16;
+      return j < uz && at < sel_end ? __ldg(sel + at / p.ratio) : -1;
+    };
+    auto token_of = [&](int j, int32_t col) -> int32_t {  // the lane's token, -1 none
+      const int32_t at = j * kUnit + warp * kSlice + r16;
+      if (j >= uz) return -1;
+      if (!SEL) return at < it.keys ? at : -1;
+      int64_t t;
+      if (at < sel_end) {
+        t = (int64_t)col * p.ratio + at % p.ratio;
+        if (col < 0 || t >= local0) return -1;
+      } else {
+        t = (int64_t)local0 + (at - sel_end);
+        if (t < 0 || at >= list_len) return -1;
+      }
+      return t < it.keys ? (int32_t)t : -1;
+    };
+    auto page_of = [&](int32_t tok) -> int32_t {
+      if (tok < 0) return 0;
+      const int32_t pg = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_tokens;
+      return __ldg(table + pg);
+    };
+    // what the next stage needs, loaded one stage (columns: two) ahead
+    int32_t col2 = SEL ? sel_entry(ua + 1) : 0;
+    int32_t tok1 = token_of(ua, SEL ? sel_entry(ua) : 0);
+    int32_t page1 = page_of(tok1);
+    auto issue = [&](int j) {  // fills the next stage with unit j's slice
+      const int st = issued % kStages;
+      const bool valid = tok1 >= 0;
+      const uint32_t vm = __ballot_sync(0xffffffffu, valid);
+      const uint32_t dst = ring_u32 + st * G::kStage + lane * G::kRow;
+      if (lane == 0) {
+        masks[st] = vm & 0xFFFFu;
+        ptx::mbar_arrive_expect_tx(&bars[st], (uint32_t)__popc(vm) * 2 * D);
+      }
+      __syncwarp();
+      if (valid) {
+        const int32_t pg = min(max(page1, 0), p.num_pages - 1);
+        const int32_t off = p.page_shift >= 0 ? tok1 & (p.page_tokens - 1) : tok1 % p.page_tokens;
+        bulk_row(dst, base + (int64_t)pg * page_stride + (int64_t)off * token_stride, 2 * D, ptx::smem_u32(&bars[st]));
+      } else if (vm != 0) {
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<uint4*>(ring + st * G::kStage + lane * G::kRow + c * 16) = make_uint4(0, 0, 0, 0);
+        ptx::fence_proxy_async_smem();  // before a later copy into the row
+      }
+      ++issued;
+      tok1 = token_of(j + 1, col2);
+      page1 = page_of(tok1);
+      if (SEL) col2 = sel_entry(j + 2);
+    };
+    for (int i = 0; i < kStages && ua + i < uz; ++i) issue(ua + i);
+    __syncthreads();  // q
+
+    uint32_t qf[MT == 1 ? D / 16 : 1][4];
+    const uint32_t q_addr =
+        ptx::smem_u32(smem + L::q) + (lane & 15) * G::kRow + (lane >> 4) * 16;  // row, 8-element half
+    if (MT == 1) {
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) ldsm4(qf[MT == 1 ? ks : 0], q_addr + ks * 32);
+    }
+    int32_t lim[MT][2];  // keys [0, lim) are seen by the thread's rows
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        lim[mt][h] = min(max(it.pos0 + 1 + (mt * 16 + h * 8 + (lane >> 2)) / gs, 0), it.keys);
+    const int32_t all_see = min(max(it.pos0 + 1, 0), it.keys);
+
+    float o[MT][D / 8][4], m[MT][2], l[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.0f;
+      m[mt][0] = m[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.0f;
+    }
+
+    for (int j = ua; j < uz; ++j) {
+      const int st = used % kStages;
+      if (ok) ok = __all_sync(0xffffffffu, wait_phase(&bars[st], (used / kStages) & 1u, abort_flag, p.fault));
+      ++used;
+      const uint32_t vm = masks[st];
+      if (ok && vm != 0) {
+        const uint32_t kb = ring_u32 + st * G::kStage;
+        float x[MT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[mt][e >> 2][e & 3] = 0.0f;
+        // keys: lanes 0-7 rows 0-7 and 16-23 rows 8-15 of 8-element half 0, the others of half 1
+        const uint32_t k_addr = kb + ((lane & 7) + ((lane >> 4) << 3)) * G::kRow + ((lane >> 3) & 1) * 16;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t bk[4];
+          ldsm4(bk, k_addr + ks * 32);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t aq[4];
+            if (MT == 1) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) aq[e] = qf[MT == 1 ? ks : 0][e];
+            } else {
+              ldsm4(aq, q_addr + mt * 16 * G::kRow + ks * 32);
+            }
+            mma16816<F16>(x[mt][0], aq, bk[0], bk[1]);
+            mma16816<F16>(x[mt][1], aq, bk[2], bk[3]);
+          }
+        }
+        const int32_t key0 = j * kUnit + warp * kSlice;
+        if (SEL ? vm != 0xFFFFu : key0 + kSlice > all_see) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int c = n * 8 + (lane & 3) * 2 + (e & 1);
+                const bool seen = SEL ? (vm >> c) & 1u : key0 + c < lim[mt][e >> 1];
+                if (!seen) x[mt][n][e] = -INFINITY;
+              }
+        }
+        uint32_t pa[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float mx = fmaxf(fmaxf(x[mt][0][2 * h], x[mt][0][2 * h + 1]), fmaxf(x[mt][1][2 * h], x[mt][1][2 * h + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            mx *= p.scale_log2;
+            if (__any_sync(0xffffffffu, mx > m[mt][h])) {
+              const float mn = fmaxf(m[mt][h], mx);
+              const float f = mn == -INFINITY ? 1.0f : ex2(m[mt][h] - mn);
+              m[mt][h] = mn;
+              l[mt][h] *= f;
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i) {
+                o[mt][i][2 * h] *= f;
+                o[mt][i][2 * h + 1] *= f;
+              }
+            }
+            const float sub = m[mt][h] == -INFINITY ? 0.0f : -m[mt][h];
+            float pr[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pr[e] = ex2(fmaf(x[mt][e >> 1][2 * h + (e & 1)], p.scale_log2, sub));
+            l[mt][h] += (pr[0] + pr[1]) + (pr[2] + pr[3]);
+            pa[mt][h] = pack2<F16>(pr[0], pr[1]);
+            pa[mt][2 + h] = pack2<F16>(pr[2], pr[3]);
+          }
+        }
+        // values: transposed loads, lanes 0-15 rows 0-15 of columns 0-7, lanes 16-31 of columns 8-15
+        const uint32_t v_addr = kb + kSlice * G::kRow + (lane & 15) * G::kRow + (lane >> 4) * 16;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t bv[4];
+          ldsm4t(bv, v_addr + i * 32);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816<F16>(o[mt][2 * i], pa[mt], bv[0], bv[1]);
+            mma16816<F16>(o[mt][2 * i + 1], pa[mt], bv[2], bv[3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (j + kStages < uz && ok) issue(j + kStages);
+    }
+    if (!ok) {  // gave up on a copy: let the others of this warp land before the memory is reused
+      for (; used < issued; ++used) {
+        const long long t0 = clock64();
+        while (!ptx::mbar_try_wait(&bars[used % kStages], (used / kStages) & 1u) && clock64() - t0 < kSpin) {
+        }
+      }
+      used = issued;
+    }
+
+    // ---- join the warps
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float t = l[mt][h];
+        t += __shfl_xor_sync(0xffffffffu, t, 1);
+        t += __shfl_xor_sync(0xffffffffu, t, 2);
+        const int r = mt * 16 + h * 8 + (lane >> 2);
+        if ((lane & 3) == 0) ml[warp * kRows + r] = make_float2(m[mt][h], t);
+        float* dst = reinterpret_cast<float*>(ring) + r * G::kMergeRow + (lane & 3) * 2;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<float2*>(dst + i * 8) = make_float2(o[mt][i][2 * h], o[mt][i][2 * h + 1]);
+      }
+    __syncthreads();
+
+    const int c = (int)blockIdx.x;
+    const int c0 = it.s0 >= s.u0 ? c : s.owner(it.s0);
+    const int c1 = it.s1 <= s.u1 ? c : s.owner(it.s1 - 1);
+    const bool split = c0 != c1;
+    float* part = p.parts + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * part_floats<D, MT>();
+    auto write_out = [&](int r, int d, float M, float Lsum, const float (&acc)[4]) {
+      const int tk = r / gs, g = r - tk * gs;
+      const int64_t row = it.row0 + tk;
+      const float inv = Lsum > 0.0f ? 1.0f / Lsum : (Lsum == 0.0f ? 0.0f : Lsum);
+      uint2 w = make_uint2(pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv));
+      *reinterpret_cast<uint2*>(p.out + row * p.out_token_stride + (int64_t)(head0 + g) * p.out_head_stride + d * 2) = w;
+      if (d == 0 && p.lse) p.lse[row * p.num_q_heads + head0 + g] = (M + log2f(Lsum)) * kLn2;
+    };
+    for (int i = tid; i < kRows * (D / 4); i += kNT) {
+      const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+      if (r >= live) continue;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * kRows + r].x);
+      float Ls = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 e = ml[w * kRows + r];
+        const float f = e.x == -INFINITY ? 0.0f : ex2(e.x - M);
+        const float4 v = *reinterpret_cast<const float4*>(
+            reinterpret_cast<const float*>(smem + w * G::kWarpBytes) + r * G::kMergeRow + d);
+        Ls += e.y * f;
+        acc[0] = fmaf(v.x, f, acc[0]);
+        acc[1] = fmaf(v.y, f, acc[1]);
+        acc[2] = fmaf(v.z, f, acc[2]);
+        acc[3] = fmaf(v.w, f, acc[3]);
+      }
+      if (!split) {
+        write_out(r, d, M, Ls, acc);
+      } else {
+        __stcg(reinterpret_cast<float4*>(part + r * D + d), make_float4(acc[0], acc[1], acc[2], acc[3]));
+        if (d == 0) __stcg(reinterpret_cast<float2*>(part + kRows * D + 2 * r), make_float2(M, Ls));
+      }
+    }
+    if (split) {
+      // ---- join the CTAs: the last one to arrive adds up the parts, in the CTAs' order
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const uint32_t n = (uint32_t)(c1 - c0 + 1);
+        const uint32_t old = atomicAdd(p.counters + c0, 1u);
+        last_sh = old + 1 == n;
+        if (old + 1 == n) p.counters[c0] = 0;  // every arrival is in: zero for the next call
+        __threadfence();
+      }
+      __syncthreads();
+      if (last_sh) {
+        auto part_of = [&](int f) { return p.parts + ((int64_t)f * 2 + (f == c0 ? 1 : 0)) * part_floats<D, MT>(); };
+        for (int i = tid; i < live * (D / 4); i += kNT) {
+          const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+          float M = -INFINITY;
+          for (int f = c0; f <= c1; ++f)
+            M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(part_of(f) + kRows * D + 2 * r)).x);
+          float Ls = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+          for (int f = c0; f <= c1; ++f) {
+            const float* pf = part_of(f);
+            const float2 e = __ldcg(reinterpret_cast<const float2*>(pf + kRows * D + 2 * r));
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(pf + r * D + d));
+            const float w = e.x == -INFINITY ? 0.0f : ex2(e.x - M);
+            Ls += e.y * w;
+            acc[0] = fmaf(v.x, w, acc[0]);
+            acc[1] = fmaf(v.y, w, acc[1]);
+            acc[2] = fmaf(v.z, w, acc[2]);
+            acc[3] = fmaf(v.w, w, acc[3]);
+          }
+          write_out(r, d, M, Ls, acc);
+        }
+      }
+    }
+    if (z == s.u1) break;
+    if (SEL) {
+      sel_item(it.s1);
+    } else {
+      walk->next();
+      it = walk->it;
+    }
+    ptx::fence_proxy_async_smem();  // the stages were written by plain stores
+    __syncthreads();
+  }
+}
+
+template <bool F16, int D, int MT, bool SEL>
+cudaError_t launch_t(const AttnParams& p, int grid, cudaStream_t stream) {
+  auto kern = attn_gather_kernel<F16, D, MT, SEL>;
+  constexpr int smem = Layout<D, MT>::total;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(kNT, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <bool F16, int D>
+cudaError_t launch_d(const AttnParams& p, int mt, int grid, cudaStream_t stream) {
+  if (p.num_selected > 0)
+    return mt == 1 ? launch_t<F16, D, 1, true>(p, grid, stream) : launch_t<F16, D, 2, true>(p, grid, stream);
+  return mt == 1 ? launch_t<F16, D, 1, false>(p, grid, stream) : launch_t<F16, D, 2, false>(p, grid, stream);
+}
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+// Counters first (one a CTA), then two parts a CTA of the larger row count.
+size_t attn_gather_workspace(int head_dim) {
+  return (size_t)kMaxGrid * 4 + (size_t)kMaxGrid * 2 * kGatherRows * (head_dim + 2) * 4;
+}
+
+cudaError_t launch_attn_gather(AttnParams p, const qsa_attn_desc& d, uint8_t* workspace, cudaStream_t stream) {
+  DeviceInfo info;
+  cudaError_t e = device_info(&info);
+  if (e != cudaSuccess) return e;
+  p.counters = reinterpret_cast<uint32_t*>(workspace);
+  p.parts = reinterpret_cast<float*>(workspace + (size_t)kMaxGrid * 4);
+  // query heads beyond what an item's rows hold become further virtual heads
+  p.splits = (p.group + kGatherRows - 1) / kGatherRows;
+  p.sub = (p.group + p.splits - 1) / p.splits;
+  p.hv = d.kv.num_kv_heads * p.splits;
+  // One 16-row tile when the expected rows fit it (the bound, else the mean),
+  // two otherwise; an item takes as many whole tokens as its rows hold.
+  int64_t toks = 1;
+  if (p.num_selected == 0)
+    toks = d.max_new > 0 ? d.max_new : (d.num_tokens + d.num_requests - 1) / d.num_requests;
+  const int mt = toks * p.sub <= 16 ? 1 : 2;
+  p.tpi = p.num_selected > 0 ? 1 : 16 * mt / p.sub;
+  p.min_units = 1;
+  const int grid = info.num_sms < kMaxGrid ? info.num_sms : kMaxGrid;
+  const bool f16 = d.kv.dtype == QSA_HALF_F16;
+  if (d.kv.head_dim == 128) return f16 ? launch_d<true, 128>(p, mt, grid, stream) : launch_d<false, 128>(p, mt, grid, stream);
+  return f16 ? launch_d<true, 64>(p, mt, grid, stream) : launch_d<false, 64>(p, mt, grid, stream);
+}
+
+}  // namespace qsa

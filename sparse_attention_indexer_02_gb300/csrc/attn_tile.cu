@@ -1,0 +1,608 @@
+// qsa_paged_attention, tile form: chunks of new tokens, on tcgen05.
+//
+// The mathematics is the gathered form's (attn_gather.cu): one pass over the
+// keys with a running maximum m, sum l and output o per row.  Here 128 query
+// rows are one MMA tile - as many whole tokens as fit, each with all query
+// heads of the key/value head, so that grouped heads share the key tile and the
+// causal edge is as wide as a few tokens only - and a CTA works on two such
+// tiles, its streams 0 and 1, against the same key and value tiles of 128 keys:
+//
+//   S = Q K^T   (128 x 128, fp32 in TMEM; Q and K from shared memory)
+//   P = 2^(S * scale * log2 e - m)   in registers, one thread a row
+//   O = O + P V (128 x D, fp32 in TMEM; P as 16-bit in TMEM over S, V from
+//                shared memory, where its rows are keys: the MN-major operand)
+//
+// TMEM is full: S/P and O of both streams are 2 * 128 + 2 * D columns.
+// What bounds a chunk is the tensor core (4 * D flop a row and key); the
+// exponentials are half its time.  The two streams exist to keep it busy: the
+// softmax of one runs while the MMAs of the other do.  Two tiles on one key
+// tile also halve what L2 has to deliver, 64 KB for 2048 cycles of MMA.
+//
+// m is not the exact running maximum: it is raised only when a row's maximum
+// passes it by more than 8 (in units of log2), since any m that keeps the
+// exponentials in range gives the same quotient o / l.  P then reaches 2^8 at
+// most, and the pass over O that raising m costs (TMEM to registers and back)
+// happens a few times a row in all, instead of a few times a tile.
+//
+// Roles: warp 0 copies (TMA: the pages of a key tile are one box each a 64-element half),
+// warp 1 issues the MMAs, warps 4-7 and 8-11 are the softmax and the epilogue
+// of stream 0 and 1.  Key and value tiles share one ring of stages.  Keys past
+// the last one a tile sees are masked in S; the values there are zeroed in
+// shared memory by the MMA warp before it uses them (up to the next multiple of
+// 16 keys, the product stops there), so nothing that a page holds past a
+// request's end enters a product.
+//
+// Schedule: equal shares of the (item, 128-key) units (attn_common.cuh).  Items
+// that lie in several CTAs leave unnormalised parts; a second, small launch
+// joins them with as many CTAs as there are rows to join (one CTA joining the
+// parts of a long item alone would take longer than the item's share).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "attn_common.cuh"
+
+namespace qsa {
+namespace umma {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // umma.cu
+}
+namespace attn {
+namespace {
+
+constexpr int kNT = 384;
+constexpr int kRows = 128;     // query rows a stream
+constexpr int kMetaWords = 8;  // of a split item: parts, first row, tokens, virtual head
+constexpr float kRaise = 8.0f;
+
+template <int D>
+struct Geo {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTile = kRows * 2 * D;          // bytes of a 128-row tile
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int q = 0;                          // two tiles
+  static constexpr int ring = 2 * kTile;
+  static constexpr int bars = ring + kStages * kTile;
+  static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 1;
+  static constexpr int misc = bars + kBars * 8;
+  static constexpr int total = 1024 + misc + 16;
+  static_assert(total <= 227 * 1024 - 1024, "shared memory (static part aside)");
+};
+
+template <int D>
+constexpr int64_t part_floats() {  // o as [D / 4][128 rows][4], then (m, l) of each row
+  return kRows * (D + 2);
+}
+
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+template <bool F16, int D>
+__global__ void __launch_bounds__(kNT, 1)
+    attn_tile_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map, const AttnParams p) {
+  using G = Geo<D>;
+  constexpr int kStages = G::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ SchedShared sched_sh;
+  uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::bars);
+  uint64_t* empty = full + kStages;
+  uint64_t* s_full = empty + kStages;   // [2] scores of a stream ready
+  uint64_t* p_ready = s_full + 2;       // [2] probabilities stored (and O raised)
+  uint64_t* o_done = p_ready + 2;       // [2] an item's last product done
+  uint64_t* q_bar = o_done + 2;         // [2] q loaded, q free
+  uint64_t* done = q_bar + 2;           // abort: the MMAs in flight are done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::misc + 4);
+  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(&full[i], 1);
+      ptx::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&s_full[i], 1);
+      ptx::mbar_init(&p_ready[i], kRows);
+      ptx::mbar_init(&o_done[i], 1);
+      ptx::mbar_init(&q_bar[i], 1);
+    }
+    ptx::mbar_init(done, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&q_map);
+    ptx::prefetch_tmap(&k_map);
+    ptx::prefetch_tmap(&v_map);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(tmem_slot, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  ptx::tc_fence_before();
+  const Schedule s = make_schedule<kNT>(p, sched_sh);  // with CTA barriers
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int tpt = p.tpi / 2;  // tokens a stream
+  const int c = (int)blockIdx.x;
+  if (threadIdx.x == 0) p.meta[c * kMetaWords] = 0;
+
+  if (s.u0 < s.u1) {
+    Walker w(p, sched_sh, s.u0);
+    if (warp == 0) {
+      // ------------------------------------------------------------ copies
+      const int box = min(p.page_tokens, kUnit);
+      uint32_t r = 0, items = 0;
+      bool ok = true;
+      for (;;) {
+        const Item& it = w.it;
+        const int ua = (int)(max(s.u0, it.s0) - it.s0), uz = (int)(min(s.u1, it.s1) - it.s0);
+        const int nst = it.n > tpt ? 2 : 1;
+        if (items > 0) ok = __all_sync(0xffffffffu, wait_phase(&q_bar[1], (items - 1) & 1u, abort_flag, p.fault));
+        if (!ok) break;
+        ++items;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&q_bar[0], (uint32_t)(nst * G::kHalves * tpt * p.group * 128));
+          for (int st = 0; st < nst; ++st)
+            for (int h = 0; h < G::kHalves; ++h)
+              ptx::tma_load_3d_plain(smem + G::q + st * G::kTile + h * (kRows * 128), &q_map, h * 64,
+                                     it.hv * p.group, it.row0 + st * tpt, &q_bar[0]);
+        }
+        const int32_t* table = p.block_table + (int64_t)it.b * p.table_stride;
+        auto page_at = [&](int j) -> int32_t {  // the page of the lane's box of key tile j
+          const int32_t t = j * kUnit + lane * box;
+          return j < uz && lane * box < kUnit && t < it.keys ? __ldg(table + t / p.page_tokens) : 0;
+        };
+        int32_t page = page_at(ua);
+        for (int j = ua; j < uz && ok; ++j) {
+          const int valid = min(kUnit, it.keys - j * kUnit);
+          const int nb = valid > 0 ? (valid + box - 1) / box : 0;
+          const int32_t pg = min(max(page, 0), p.num_pages - 1);
+          page = page_at(j + 1);
+          const int off = (j * kUnit + lane * box) % p.page_tokens;
+          for (int kv = 0; kv < 2 && ok; ++kv, ++r) {
+            const int st = r % kStages;
+            ok = __all_sync(0xffffffffu, wait_phase(&empty[st], ((r / kStages) & 1u) ^ 1u, abort_flag, p.fault));
+            if (!ok) break;
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(nb * box * 128 * G::kHalves));
+            __syncwarp();
+            if (lane < nb)
+              for (int h = 0; h < G::kHalves; ++h)
+                ptx::tma_load_4d(smem + G::ring + st * G::kTile + h * (kRows * 128) + lane * box * 128,
+                                 kv ? &v_map : &k_map, h * 64, off, it.hv, pg, &full[st]);
+          }
+        }
+        if (!ok || it.s1 >= s.u1) break;
+        w.next();
+      }
+      if (*abort_flag) {  // copies in flight land before the CTA ends
+        for (uint32_t i = r > kStages ? r - kStages : 0; i < r; ++i) {
+          const long long t0 = clock64();
+          while (!ptx::mbar_try_wait(&full[i % kStages], (i / kStages) & 1u) && clock64() - t0 < kSpin) {
+          }
+        }
+        if (items > 0) {
+          const long long t0 = clock64();
+          while (!ptx::mbar_try_wait(&q_bar[0], (items - 1) & 1u) && clock64() - t0 < kSpin) {
+          }
+        }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ products
+      constexpr uint32_t id_qk = F16 ? ptx::idesc_f16_f32(128, 128) : ptx::idesc_bf16_f32(128, 128);
+      constexpr uint32_t id_pv = (F16 ? ptx::idesc_f16_f32(128, D) : ptx::idesc_bf16_f32(128, D)) | ptx::kIdescBMnMajor;
+      const uint32_t q_u32 = ptx::smem_u32(smem + G::q), ring_u32 = ptx::smem_u32(smem + G::ring);
+      uint32_t r = 0, items = 0, tiles[2] = {0, 0};
+      bool ok = true;
+      auto wwait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_phase(bar, parity, abort_flag, p.fault));
+      };
+      auto qk = [&](int st, int stage) {
+        const uint64_t a = ptx::sw128_desc(q_u32 + st * G::kTile), b = ptx::sw128_desc(ring_u32 + stage * G::kTile);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint64_t o = (uint64_t)(((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4);
+          ptx::mma_bf16_elect(tmem + st * 128, a + o, b + o, id_qk, ks > 0);
+        }
+        ptx::mma_commit_elect(&s_full[st]);
+      };
+      for (; ok;) {
+        const Item& it = w.it;
+        const int ua = (int)(max(s.u0, it.s0) - it.s0), uz = (int)(min(s.u1, it.s1) - it.s0);
+        const int nst = it.n > tpt ? 2 : 1;
+        ok = wwait(&q_bar[0], items & 1u) && wwait(&full[r % kStages], (r / kStages) & 1u);
+        if (!ok) break;
+        ++items;
+        ptx::tc_fence_after();
+        for (int st = 0; st < nst; ++st) qk(st, r % kStages);
+        ptx::mma_commit_elect(&empty[r % kStages]);
+        ++r;
+        for (int j = ua; j < uz && ok; ++j, r += 2) {  // r: the value tile of j; r + 1: the key tile of j + 1
+          const int vst = r % kStages, kst = (r + 1) % kStages;
+          const bool more = j + 1 < uz;
+          ok = wwait(&full[vst], (r / kStages) & 1u);
+          if (!ok) break;
+          const int valid = max(0, min(kUnit, it.keys - j * kUnit));
+          const int steps = (valid + 15) / 16;
+          if (valid & 15) {  // zero the value rows between the last key and the product's end
+            uint8_t* v = smem + G::ring + vst * G::kTile;
+            const int rows = steps * 16 - valid;
+            for (int i = lane; i < rows * 8 * G::kHalves; i += 32)
+              *reinterpret_cast<uint4*>(v + (i / (rows * 8)) * (kRows * 128) + valid * 128 + (i % (rows * 8)) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+          }
+          const uint64_t vd = ptx::sw128_mn_desc(ring_u32 + vst * G::kTile, kRows * 128);
+          for (int st = 0; st < nst; ++st) {
+            ok = wwait(&p_ready[st], tiles[st] & 1u);
+            if (!ok) break;
+            ++tiles[st];
+            ptx::tc_fence_after();
+            for (int ks = 0; ks < steps; ++ks)
+              ptx::mma_bf16_ts_elect(tmem + 256 + st * D, tmem + st * 128 + ks * 8, vd + (uint64_t)(ks * (2048 >> 4)),
+                                     id_pv, j > ua || ks > 0);
+            if (!more) ptx::mma_commit_elect(&o_done[st]);
+            if (st == nst - 1) ptx::mma_commit_elect(&empty[vst]);
+            if (more) {
+              if (st == 0) {
+                ok = wwait(&full[kst], ((r + 1) / kStages) & 1u);
+                if (!ok) break;
+                ptx::tc_fence_after();
+              }
+              qk(st, kst);
+              if (st == nst - 1) ptx::mma_commit_elect(&empty[kst]);
+            }
+          }
+        }
+        // the loop left r one past the next key tile: the item's last value tile was r - 2
+        r -= 1;
+        if (!ok) break;
+        ptx::mma_commit_elect(&q_bar[1]);
+        if (it.s1 >= s.u1) break;
+        w.next();
+      }
+      if (!ok) {
+        ptx::mma_commit_elect(done);
+        const long long t0 = clock64();
+        while (!ptx::mbar_try_wait(done, 0) && clock64() - t0 < kSpin) {
+        }
+      }
+    } else if (warp >= 4) {
+      // ------------------------------------------------------------ softmax and epilogue
+      const int st = (warp - 4) >> 2;
+      const int row = ((warp & 3) << 5) + lane;
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t t_s = tmem + lanes + st * 128, t_o = tmem + lanes + 256 + st * D;
+      const float sc = p.scale_log2;
+      const uint64_t sc2 = pack_f32x2(sc, sc);
+      const float raise = kRaise / sc;  // in units of S
+      uint32_t tiles = 0, items = 0;
+      bool ok = true;
+      for (;;) {
+        const Item& it = w.it;
+        const int ua = (int)(max(s.u0, it.s0) - it.s0), uz = (int)(min(s.u1, it.s1) - it.s0);
+        const int n = min(it.n - st * tpt, tpt);  // tokens of this stream
+        if (n > 0) {
+          const int tk = row / p.group;
+          const int32_t lim = min(max(it.pos0 + st * tpt + tk + 1, 0), it.keys);  // keys [0, lim) are seen
+          float m = -INFINITY, l = 0.0f;  // m in units of S
+          for (int j = ua; j < uz; ++j, ++tiles) {
+            ok = __all_sync(0xffffffffu, wait_phase(&s_full[st], tiles & 1u, abort_flag, p.fault));
+            if (!ok) break;
+            ptx::tc_fence_after();
+            uint32_t x[4][32];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ptx::tmem_ld32(t_s + q * 32, x[q]);
+            ptx::tmem_ld_wait();
+            const int seen = lim - j * kUnit;
+            if (__any_sync(0xffffffffu, seen < kUnit)) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (q * 32 + i >= seen) x[q][i] = 0xFF800000u;
+            }
+            float mx[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              mx[q] = __uint_as_float(x[q][0]);
+#pragma unroll
+              for (int i = 1; i < 32; ++i) mx[q] = fmaxf(mx[q], __uint_as_float(x[q][i]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // raise m (for m = -inf: to any maximum)
+            if (__any_sync(0xffffffffu, top > m + raise || (m == -INFINITY && top > m))) {
+              const float mn = fmaxf(m, top);
+              const float f = mn == -INFINITY ? 1.0f : ex2((m - mn) * sc);
+              m = mn;
+              l *= f;
+              if (j > ua) {  // the stream's product before this S is done: O holds it
+#pragma unroll 1
+                for (int q = 0; q < D / 32; ++q) {
+                  uint32_t o[32];
+                  ptx::tmem_ld32(t_o + q * 32, o);
+                  ptx::tmem_ld_wait();
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  ptx::tmem_st32(t_o + q * 32, o);
+                }
+              }
+            }
+            const float neg = m == -INFINITY ? 0.0f : -m * sc;
+            const uint64_t neg2 = pack_f32x2(neg, neg);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint32_t pk[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const uint32_t* xs = &x[2 * q + (i >> 4)][(2 * i) & 31];
+                float a, b;
+                unpack_f32x2(fma2(pack_f32x2(__uint_as_float(xs[0]), __uint_as_float(xs[1])), sc2, neg2), a, b);
+                a = ex2(a);
+                b = ex2(b);
+                sum[i & 1] = add2(sum[i & 1], pack_f32x2(a, b));
+                pk[i] = pack2<F16>(a, b);
+              }
+              ptx::tmem_st32(t_s + q * 32, pk);
+            }
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&p_ready[st]);
+            float a, b;
+            unpack_f32x2(add2(sum[0], sum[1]), a, b);
+            l += a + b;
+          }
+          if (ok) ok = __all_sync(0xffffffffu, wait_phase(&o_done[st], items & 1u, abort_flag, p.fault));
+          ++items;
+          if (ok) {
+            ptx::tc_fence_after();
+            const int c0 = it.s0 >= s.u0 ? c : s.owner(it.s0);
+            const int c1 = it.s1 <= s.u1 ? c : s.owner(it.s1 - 1);
+            const bool live = tk < n && row < tpt * p.group;
+            const int64_t qrow = it.row0 + st * tpt + tk;
+            const int head = it.hv * p.group + (row - tk * p.group);
+            if (c0 == c1) {
+              const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+              uint8_t* dst = p.out + qrow * p.out_token_stride + (int64_t)head * p.out_head_stride;
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[32];
+                ptx::tmem_ld32(t_o + q * 32, o);
+                ptx::tmem_ld_wait();
+                if (live) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    uint32_t e[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                      // a row that sees nothing has l = 0 and its O is 0 * V: written as zero
+                      const float a = __uint_as_float(o[8 * i + 2 * k]) * inv, b = __uint_as_float(o[8 * i + 2 * k + 1]) * inv;
+                      e[k] = pack2<F16>(l == 0.0f ? 0.0f : a, l == 0.0f ? 0.0f : b);
+                    }
+                    *reinterpret_cast<uint4*>(dst + q * 64 + i * 16) = make_uint4(e[0], e[1], e[2], e[3]);
+                  }
+                }
+              }
+              if (live && p.lse) p.lse[qrow * p.num_q_heads + head] = (m * sc + log2f(l)) * kLn2;
+            } else {
+              float* part = p.parts + (((int64_t)c * 2 + (c == c0 ? 1 : 0)) * 2 + st) * part_floats<D>();
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[32];
+                ptx::tmem_ld32(t_o + q * 32, o);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  *reinterpret_cast<uint4*>(part + ((q * 8 + i) * kRows + row) * 4) =
+                      l == 0.0f ? make_uint4(0, 0, 0, 0) : make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              }
+              *reinterpret_cast<float2*>(part + kRows * D + 2 * row) = make_float2(m * sc, l);
+              if (c == c0 && st == 0 && row == 0) {
+                int32_t* meta = p.meta + c * kMetaWords;
+                meta[1] = it.row0;
+                meta[2] = it.n;
+                meta[3] = it.hv;
+                meta[0] = c1 - c0 + 1;
+              }
+            }
+            ptx::tc_fence_before();  // O read before the next item's products (through p_ready)
+          }
+        }
+        if (!ok || it.s1 >= s.u1) break;
+        w.next();
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 1) ptx::tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the items that lie in several CTAs: block (c0, stream, 32
+// rows) for the item that begins in CTA c0's share and ends in a later one.
+// Threads: a row each lane, the warps share out the output's float4 columns,
+// so parts are read 512 contiguous bytes a warp.
+template <bool F16, int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  const int c0 = (int)blockIdx.x, st = (int)blockIdx.y;
+  const int32_t* meta = p.meta + c0 * kMetaWords;
+  const int nf = meta[0];
+  if (nf == 0) return;
+  const int tpt = p.tpi / 2;
+  const int n = min(meta[2] - st * tpt, tpt);
+  const int row = (int)blockIdx.z * 32 + ((int)threadIdx.x & 31), warp = (int)threadIdx.x >> 5;
+  const int tk = row / p.group;
+  if (tk >= n) return;
+  const int64_t qrow = meta[1] + st * tpt + tk;
+  const int head = meta[3] * p.group + (row - tk * p.group);
+  auto part_of = [&](int f) {
+    return p.parts + (((int64_t)(c0 + f) * 2 + (f == 0 ? 1 : 0)) * 2 + st) * part_floats<D>();
+  };
+  float M = -INFINITY, L = 0.0f;
+#pragma unroll 4
+  for (int f = 0; f < nf; ++f) M = fmaxf(M, reinterpret_cast<const float2*>(part_of(f) + kRows * D)[row].x);
+  constexpr int kPer = D / 32;  // float4 columns a warp
+  float4 acc[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) acc[i] = make_float4(0, 0, 0, 0);
+#pragma unroll 2
+  for (int f = 0; f < nf; ++f) {
+    const float* pf = part_of(f);
+    const float2 e = reinterpret_cast<const float2*>(pf + kRows * D)[row];
+    const float w = e.x == -INFINITY ? 0.0f : ex2(e.x - M);
+    L += e.y * w;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const float4 v = reinterpret_cast<const float4*>(pf)[(warp + 8 * i) * kRows + row];
+      acc[i].x = fmaf(v.x, w, acc[i].x);
+      acc[i].y = fmaf(v.y, w, acc[i].y);
+      acc[i].z = fmaf(v.z, w, acc[i].z);
+      acc[i].w = fmaf(v.w, w, acc[i].w);
+    }
+  }
+  const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
+  uint8_t* dst = p.out + qrow * p.out_token_stride + (int64_t)head * p.out_head_stride;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    *reinterpret_cast<uint2*>(dst + (warp + 8 * i) * 8) =
+        make_uint2(pack2<F16>(acc[i].x * inv, acc[i].y * inv), pack2<F16>(acc[i].z * inv, acc[i].w * inv));
+  if (warp == 0 && p.lse) p.lse[qrow * p.num_q_heads + head] = (M + log2f(L)) * kLn2;
+}
+
+template <bool F16, int D>
+cudaError_t launch_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p, int grid,
+                     cudaStream_t stream) {
+  auto kern = attn_tile_kernel<F16, D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::total);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(kNT, 1, 1);
+  cfg.dynamicSmemBytes = Geo<D>::total;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, qm, km, vm, p);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)grid, 2, kRows / 32);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<F16, D>, p);
+}
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+bool attn_tile_supports(const qsa_attn_desc& d, const char** why) {
+  const int pt = d.kv.page_tokens;
+  if (d.num_selected > 0) {
+    *why = "selected columns take the gathered form";
+    return false;
+  }
+  if (pt % 8 != 0 || !(kUnit % pt == 0 || pt % kUnit == 0)) {
+    *why = "page_tokens must be 8, 16, 32, 64 or a multiple of 128";
+    return false;
+  }
+  if (d.num_q_heads / d.kv.num_kv_heads > kRows) {
+    *why = "more than 128 query heads a key/value head";
+    return false;
+  }
+  const int64_t s[] = {d.kv.k_page_stride, d.kv.k_token_stride, d.kv.k_head_stride, d.kv.v_page_stride,
+                       d.kv.v_token_stride, d.kv.v_head_stride, d.q_token_stride, d.q_head_stride};
+  for (int64_t v : s)
+    if (v >= (1LL << 40)) {
+      *why = "a stride of 2^40 bytes or more";
+      return false;
+    }
+  return true;
+}
+
+// The gathered form's counters (not touched here: one workspace serves both
+// forms in turn), two parts a CTA of both streams, the joining launch's list.
+size_t attn_tile_workspace(int head_dim) {
+  return (size_t)kMaxGrid * 4 + (size_t)kMaxGrid * 4 * kRows * (head_dim + 2) * 4 + (size_t)kMaxGrid * kMetaWords * 4;
+}
+
+cudaError_t launch_attn_tile(AttnParams p, const qsa_attn_desc& d, uint8_t* workspace, cudaStream_t stream,
+                             const char** msg) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = umma::tensor_map_encoder();
+  if (!enc) {
+    *msg = "cuTensorMapEncodeTiled is unavailable from the driver";
+    return cudaErrorInvalidValue;
+  }
+  DeviceInfo info;
+  cudaError_t e = device_info(&info);
+  if (e != cudaSuccess) return e;
+  const int D = d.kv.head_dim;
+  const bool f16 = d.kv.dtype == QSA_HALF_F16;
+  p.parts = reinterpret_cast<float*>(workspace + (size_t)kMaxGrid * 4);
+  p.meta = reinterpret_cast<int32_t*>(workspace + (size_t)kMaxGrid * 4 + (size_t)kMaxGrid * 4 * kRows * (D + 2) * 4);
+  p.splits = 1;
+  p.sub = p.group;
+  p.hv = d.kv.num_kv_heads;
+  const int tpt = kRows / p.group;
+  p.tpi = 2 * tpt;
+  p.min_units = 2;
+  const CUtensorMapDataType ty = f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUtensorMap qm, km, vm;
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)d.num_q_heads, (cuuint64_t)d.num_tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)d.q_head_stride, (cuuint64_t)d.q_token_stride};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)tpt};
+    if (enc(&qm, ty, 3, const_cast<uint8_t*>(p.q), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+      *msg = "q tensor map rejected by the driver";
+      return cudaErrorInvalidValue;
+    }
+  }
+  const int box_rows = p.page_tokens < kUnit ? p.page_tokens : kUnit;
+  for (int kv = 0; kv < 2; ++kv) {
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.page_tokens, (cuuint64_t)d.kv.num_kv_heads,
+                                (cuuint64_t)p.num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)(kv ? p.v_token_stride : p.k_token_stride),
+                                   (cuuint64_t)(kv ? p.v_head_stride : p.k_head_stride),
+                                   (cuuint64_t)(kv ? p.v_page_stride : p.k_page_stride)};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
+    if (enc(kv ? &vm : &km, ty, 4, const_cast<uint8_t*>(kv ? p.v : p.k), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+      *msg = "key/value tensor map rejected by the driver";
+      return cudaErrorInvalidValue;
+    }
+  }
+  const int grid = info.num_sms < kMaxGrid ? info.num_sms : kMaxGrid;
+  if (D == 128) return f16 ? launch_t<true, 128>(qm, km, vm, p, grid, stream) : launch_t<false, 128>(qm, km, vm, p, grid, stream);
+  return f16 ? launch_t<true, 64>(qm, km, vm, p, grid, stream) : launch_t<false, 64>(qm, km, vm, p, grid, stream);
+}
+
+}  // namespace qsa

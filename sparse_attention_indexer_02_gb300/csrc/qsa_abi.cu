@@ -55,6 +55,14 @@ qsa_status validate_desc(const qsa_paged_desc* d) {
 
 namespace qsa {
 
+qsa_status set_error(qsa_status st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
+  va_end(ap);
+  return st;
+}
+
 cudaError_t device_info(DeviceInfo* info) {
   static std::mutex mu;
   static DeviceInfo cache[64];

@@ -68,6 +68,74 @@ struct DeviceInfo {
 };
 cudaError_t device_info(DeviceInfo* info);
 
+// Records this thread's last error and returns `st` (qsa_abi.cu).
+qsa_status set_error(qsa_status st, const char* fmt, ...);
+
+// page_maps.cu
+struct PageMapsParams {
+  const int32_t *context_lens, *new_lens, *free_pages;
+  int32_t *block_table, *query_start, *seq_lens;
+  int64_t* slots;
+  int32_t *positions, *token_request, *visible_cols;  // may be null
+  int64_t* column_slots;                              // may be null
+  int32_t* pages_used;                                // may be null
+  int64_t table_stride, num_free, max_tokens;
+  int32_t num_requests, page_tokens, max_pages, ratio, partial_cols;
+};
+cudaError_t launch_page_maps(const PageMapsParams& p, cudaStream_t stream);
+
+// kv_store.cu
+struct StoreKvParams {
+  const uint8_t *k, *v;
+  const int64_t* slots;
+  uint8_t *k_cache, *v_cache;
+  int64_t k_row_stride, k_row_head_stride, v_row_stride, v_row_head_stride;
+  int64_t k_page_stride, k_token_stride, k_head_stride, v_page_stride, v_token_stride, v_head_stride;
+  int64_t num_tokens, num_slots;
+  int32_t page_tokens, num_kv_heads, head_chunks;  // head_chunks: 16-byte chunks of a head's row
+};
+cudaError_t launch_store_kv(const StoreKvParams& p, cudaStream_t stream);
+struct StoreIndexParams {
+  const uint8_t* keys;
+  const int64_t* slots;
+  uint8_t *cache, *scales;
+  int64_t row_stride, key_page_stride, scale_page_stride, num_tokens, num_slots;
+  int32_t page_cols, fp8, wide;  // wide: every key of the cache is 8-byte aligned
+};
+cudaError_t launch_store_index(const StoreIndexParams& p, cudaStream_t stream);
+
+// attn_gather.cu, attn_tile.cu: qsa_paged_attention.
+struct AttnParams {
+  const uint8_t *q, *k, *v;
+  uint8_t* out;
+  float* lse;                 // may be null
+  const int32_t *block_table, *query_start, *seq_lens, *selected;
+  float* parts;               // unfinished parts of split items
+  uint32_t* counters;         // arrivals at split items (zero between calls)
+  int32_t* meta;              // tile form: the split items, for the joining launch
+  unsigned int* fault;
+  int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+  int64_t k_page_stride, k_token_stride, k_head_stride, v_page_stride, v_token_stride, v_head_stride;
+  int64_t table_stride;
+  int32_t num_requests, num_tokens, num_q_heads, max_pages, num_pages, page_tokens, page_shift;
+  int32_t capacity;           // max_pages * page_tokens, at most kMaxKeys
+  int32_t group;              // query heads of a key/value head
+  int32_t hv, splits, sub;    // virtual heads = kv heads * splits, of `sub` query heads each
+  int32_t tpi;                // tokens an item
+  int32_t min_units;          // least units a CTA takes
+  int32_t num_selected, ratio, local_tokens;
+  float scale_log2;           // scale * log2(e)
+};
+constexpr int64_t kMaxKeys = 0x7FFFFC00;  // keys of a request (room for rounding up in 32 bits)
+// Query rows of a key/value head above which a call takes tiles.
+constexpr int kGatherRows = 32;
+size_t attn_gather_workspace(int head_dim);
+size_t attn_tile_workspace(int head_dim);
+bool attn_tile_supports(const qsa_attn_desc& d, const char** why);
+cudaError_t launch_attn_gather(AttnParams p, const qsa_attn_desc& d, uint8_t* workspace, cudaStream_t stream);
+cudaError_t launch_attn_tile(AttnParams p, const qsa_attn_desc& d, uint8_t* workspace, cudaStream_t stream,
+                             const char** msg);
+
 // page_stream.cu: qsa_page_stream's launch (arguments already validated).
 cudaError_t launch_page_stream(const uint8_t* base, int64_t page_stride, int32_t page_bytes, const int32_t* pages,
                                int64_t num_listed, int64_t pool_pages, uint32_t* checksum, cudaStream_t stream);
