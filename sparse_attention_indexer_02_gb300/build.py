@@ -1,4 +1,5 @@
-"""Builds libqsa.so in-tree with nvcc for sm_103a (no cmake, no torch extension).
+"""Builds libqsa.so in-tree with nvcc for sm_103a, and _qsa_torch, the Python
+module that calls it with torch tensors (no cmake, no extension framework).
 
 Each .cu in csrc/ compiles to an object in parallel; the objects link into one
 shared library with the CUDA runtime linked statically, so the library loads
@@ -20,6 +21,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqsa.so")
+BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
+BINDING = os.path.join(PKG, "_qsa_torch.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -47,6 +50,60 @@ def up_to_date() -> bool:
         return False
     t = os.path.getmtime(LIB)
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def _torch_stamp() -> str:
+    """What the binding was compiled against: torch's version and Python's."""
+    import torch
+
+    return f"{torch.__version__} {sys.version}"
+
+
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING):
+        return False
+    t = os.path.getmtime(BINDING)
+    try:
+        with open(os.path.join(BUILD, "binding_stamp")) as f:
+            if f.read() != _torch_stamp():
+                return False
+    except OSError:
+        return False
+    return all(os.path.getmtime(f) <= t for f in (BINDING_SRC, os.path.join(INCLUDE, "qsa.h"), os.path.abspath(__file__)))
+
+
+def _compile_binding() -> str:
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    obj = os.path.join(BUILD, "torch_binding.o")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-Wno-psabi",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-isystem{root}/include", f"-isystem{root}/include/torch/csrc/api/include", f"-isystem{cuda}/include",
+           f"-isystem{sysconfig.get_paths()['include']}", "-c", BINDING_SRC, "-o", obj]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on torch_binding.cpp:\n{res.stderr[-4000:]}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "lib64")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-shared", obj, LIB, f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python", f"-L{cuda}", "-lcudart", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}", "-o", tmp]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"link of _qsa_torch.so failed:\n{res.stderr[-4000:]}")
+    os.replace(tmp, BINDING)
+    with open(os.path.join(BUILD, "binding_stamp"), "w") as f:
+        f.write(_torch_stamp())
 
 
 def _raise_stack_limit():
@@ -93,24 +150,34 @@ def o0_units() -> list:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
+    lib_ok, binding_ok = not force and up_to_date(), not force and binding_up_to_date()
+    if lib_ok and binding_ok:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    srcs = [] if lib_ok else _sources()
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(16, os.cpu_count() or 8))) as ex:
+        binding = ex.submit(_compile_binding) if not binding_ok else None
         done = list(ex.map(_compile, srcs))
+    if not lib_ok:
+        _link_lib(done)
+    if binding is not None:
+        _link_binding(binding.result())
+    if verbose:
+        print(f"built {LIB}")
+    return LIB
+
+
+def _link_lib(done) -> None:
     objs = [o for o, _ in done]
     with open(O0_RECORD, "w") as f:
         json.dump(sorted(u for _, u in done if u), f)
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-Xcompiler", "-fPIC", *objs, "-o", tmp]
+    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-Xcompiler", "-fPIC",
+           "-Xlinker", "-soname=libqsa.so", *objs, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link of libqsa.so failed:\n{res.stderr[-4000:]}")
     os.replace(tmp, LIB)
-    if verbose:
-        print(f"built {LIB}")
-    return LIB
 
 
 if __name__ == "__main__":

@@ -492,10 +492,11 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
 }
 
 template <bool F16, int D, int MT, bool SEL>
-cudaError_t launch_t(const AttnParams& p, int grid, cudaStream_t stream) {
+cudaError_t launch_t(const AttnParams& p, int device, int grid, cudaStream_t stream) {
   auto kern = attn_gather_kernel<F16, D, MT, SEL>;
   constexpr int smem = Layout<D, MT>::total;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(kern, smem, device, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
@@ -511,10 +512,10 @@ cudaError_t launch_t(const AttnParams& p, int grid, cudaStream_t stream) {
 }
 
 template <bool F16, int D>
-cudaError_t launch_d(const AttnParams& p, int mt, int grid, cudaStream_t stream) {
+cudaError_t launch_d(const AttnParams& p, int mt, int device, int grid, cudaStream_t stream) {
   if (p.num_selected > 0)
-    return mt == 1 ? launch_t<F16, D, 1, true>(p, grid, stream) : launch_t<F16, D, 2, true>(p, grid, stream);
-  return mt == 1 ? launch_t<F16, D, 1, false>(p, grid, stream) : launch_t<F16, D, 2, false>(p, grid, stream);
+    return mt == 1 ? launch_t<F16, D, 1, true>(p, device, grid, stream) : launch_t<F16, D, 2, true>(p, device, grid, stream);
+  return mt == 1 ? launch_t<F16, D, 1, false>(p, device, grid, stream) : launch_t<F16, D, 2, false>(p, device, grid, stream);
 }
 
 }  // namespace
@@ -547,8 +548,8 @@ cudaError_t launch_attn_gather(AttnParams p, const qsa_attn_desc& d, uint8_t* wo
   p.min_units = 1;
   const int grid = info.num_sms < kMaxGrid ? info.num_sms : kMaxGrid;
   const bool f16 = d.kv.dtype == QSA_HALF_F16;
-  if (d.kv.head_dim == 128) return f16 ? launch_d<true, 128>(p, mt, grid, stream) : launch_d<false, 128>(p, mt, grid, stream);
-  return f16 ? launch_d<true, 64>(p, mt, grid, stream) : launch_d<false, 64>(p, mt, grid, stream);
+  if (d.kv.head_dim == 128) return f16 ? launch_d<true, 128>(p, mt, info.device, grid, stream) : launch_d<false, 128>(p, mt, info.device, grid, stream);
+  return f16 ? launch_d<true, 64>(p, mt, info.device, grid, stream) : launch_d<false, 64>(p, mt, info.device, grid, stream);
 }
 
 }  // namespace qsa

@@ -493,10 +493,11 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
 }
 
 template <bool F16, int D>
-cudaError_t launch_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p, int grid,
-                     cudaStream_t stream) {
+cudaError_t launch_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p, int device,
+                     int grid, cudaStream_t stream) {
   auto kern = attn_tile_kernel<F16, D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::total);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(kern, Geo<D>::total, device, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
@@ -601,8 +602,8 @@ cudaError_t launch_attn_tile(AttnParams p, const qsa_attn_desc& d, uint8_t* work
     }
   }
   const int grid = info.num_sms < kMaxGrid ? info.num_sms : kMaxGrid;
-  if (D == 128) return f16 ? launch_t<true, 128>(qm, km, vm, p, grid, stream) : launch_t<false, 128>(qm, km, vm, p, grid, stream);
-  return f16 ? launch_t<true, 64>(qm, km, vm, p, grid, stream) : launch_t<false, 64>(qm, km, vm, p, grid, stream);
+  if (D == 128) return f16 ? launch_t<true, 128>(qm, km, vm, p, info.device, grid, stream) : launch_t<false, 128>(qm, km, vm, p, info.device, grid, stream);
+  return f16 ? launch_t<true, 64>(qm, km, vm, p, info.device, grid, stream) : launch_t<false, 64>(qm, km, vm, p, info.device, grid, stream);
 }
 
 }  // namespace qsa

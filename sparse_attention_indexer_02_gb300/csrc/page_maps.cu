@@ -142,7 +142,8 @@ cudaError_t launch_page_maps(const PageMapsParams& p, cudaStream_t stream) {
   cudaError_t e = device_info(&info);
   if (e != cudaSuccess) return e;
   const size_t smem = (size_t)(p.num_requests + 1) * 8;
-  e = cudaFuncSetAttribute(page_maps_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> allowed{0};
+  e = allow_smem(page_maps_kernel, (kMaxMapRequests + 1) * 8, info.device, allowed);
   if (e != cudaSuccess) return e;
   const int64_t work = p.max_tokens > p.num_requests + 1 ? p.max_tokens : p.num_requests + 1;
   const int64_t want = (work + kNT - 1) / kNT;

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/qsa.h"
 
 namespace qsa {
@@ -68,10 +70,23 @@ struct DeviceInfo {
 };
 cudaError_t device_info(DeviceInfo* info);
 
+// Raises a kernel's dynamic shared memory limit to `bytes`, on the first call
+// for a device (`done`: one bit a device, one word a kernel).  A call every
+// launch costs about a microsecond of host time.
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, int device, std::atomic<uint64_t>& done) {
+  const bool known = device >= 0 && device < 64;
+  if (known && (done.load(std::memory_order_acquire) >> device & 1)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) done.fetch_or(1ull << device, std::memory_order_release);
+  return e;
+}
+
 // Records this thread's last error and returns `st` (qsa_abi.cu).
 qsa_status set_error(qsa_status st, const char* fmt, ...);
 
 // page_maps.cu
+constexpr int kMaxMapRequests = 16384;  // their two sums fit a CTA's shared memory
 struct PageMapsParams {
   const int32_t *context_lens, *new_lens, *free_pages;
   int32_t *block_table, *query_start, *seq_lens;

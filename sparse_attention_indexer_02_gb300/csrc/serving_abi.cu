@@ -91,7 +91,8 @@ qsa_status qsa_build_page_maps(const qsa_page_maps_desc* d, const int32_t* conte
                                int32_t* visible_cols, int64_t* column_slots, int32_t* pages_used, void* stream) {
   if (!d) return bad("desc is NULL");
   if (d->num_requests < 0) return bad("num_requests < 0");
-  if (d->num_requests > 16384) return set_error(QSA_ERR_UNSUPPORTED, "num_requests > 16384");
+  if (d->num_requests > qsa::kMaxMapRequests)
+    return set_error(QSA_ERR_UNSUPPORTED, "num_requests > %d", qsa::kMaxMapRequests);
   if (d->page_tokens < 1) return bad("page_tokens < 1");
   if (d->max_pages < 1) return bad("max_pages < 1");
   if ((int64_t)d->max_pages * d->page_tokens > 0x7FFFFFFFLL) return bad("max_pages * page_tokens exceeds 2^31 - 1");

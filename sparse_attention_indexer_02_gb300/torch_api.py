@@ -6,12 +6,29 @@ device; work is enqueued on the current torch stream unless one is given.
 """
 from __future__ import annotations
 
-import contextlib
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import _abi
+
+
+class _Binding:
+    """The module _qsa_torch, loaded by its first use; loud when it is missing."""
+
+    def __getattr__(self, name):
+        _abi.load_library()  # _qsa_torch links against libqsa.so
+        try:
+            from . import _qsa_torch as mod
+        except ImportError as e:
+            raise RuntimeError("_qsa_torch is not built for this torch: run "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        for n in ("build_page_maps", "store_paged_kv", "store_index_keys", "paged_attention"):
+            setattr(self, n, getattr(mod, n))
+        return getattr(mod, name)
+
+
+_qsa_torch = _Binding()
 
 
 def _desc_from(q, kv_cache, block_table, page_cols, out_cols, kv_dtype, scale_offset):
@@ -122,44 +139,14 @@ def paged_mqa_topk(q: torch.Tensor, weights: torch.Tensor, kv_cache: torch.Tenso
 
 
 # ---- serving operators: page maps, paged stores, paged attention -------------
-
-_HALF = {torch.bfloat16: _abi.HALF_BF16, torch.float16: _abi.HALF_F16}
-
+# Checked and called from _qsa_torch (csrc/torch_binding.cpp): tensors that do
+# not fit a call raise ValueError, a status of the C ABI other than OK QSAError.
 
 def _on(stream):
-    """Context in which tensors a call allocates belong to the stream it runs on."""
-    if stream is None:
-        return contextlib.nullcontext()
+    """Context in which a call's launches and allocations belong to `stream`."""
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
     return torch.cuda.stream(stream)
-
-
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
-
-
-def _vec(t: torch.Tensor, name: str, dtype: torch.dtype, *shape: int) -> None:
-    _need(t.dtype == dtype and t.dim() == len(shape) and t.is_contiguous() and
-          all(n < 0 or t.shape[i] == n for i, n in enumerate(shape)),
-          f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} (-1: any), "
-          f"got {t.dtype} {list(t.shape)} strides {list(t.stride())}")
-
-
-def _table(t: torch.Tensor) -> None:
-    _need(t.dtype == torch.int32 and t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1),
-          "block_table must be an int32 [num_requests, max_pages] tensor with contiguous rows")
-
-
-def _strides(t: torch.Tensor) -> list:
-    """Element strides with those of dimensions of one entry, which may be
-    anything, set to what a contiguous tensor has."""
-    out, inner = [], 1
-    for n, st in zip(reversed(t.shape), reversed(t.stride())):
-        out.append(st if n > 1 else inner)
-        inner *= max(n, 1)
-    return out[::-1]
 
 
 class PageMaps(NamedTuple):
@@ -180,48 +167,19 @@ def build_page_maps(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pag
     """Page bookkeeping of one step on the device (include/qsa.h,
     qsa_build_page_maps): block_table is extended in place with pages of
     free_pages, the rest is returned (or written into `out`, a PageMaps whose
-    tensors a captured graph keeps).  context_lens, new_lens: int32 [B];
-    free_pages: int32; block_table: int32 [B, max_pages]; max_tokens: rows of
-    the per-token outputs (padding past the step's tokens)."""
-    B = context_lens.numel()
-    _vec(context_lens, "context_lens", torch.int32, -1)
-    _vec(new_lens, "new_lens", torch.int32, B)
-    _vec(free_pages, "free_pages", torch.int32, -1)
-    _table(block_table)
-    _need(block_table.shape[0] == B, "block_table must have a row a request")
-    _need(max_tokens >= 0, "max_tokens < 0")
-    if out is None:
-        dev = context_lens.device
+    tensors a captured graph keeps; new ones share one allocation).
+    context_lens, new_lens: int32 [B]; free_pages: int32; block_table: int32
+    [B, max_pages]; max_tokens: rows of the per-token outputs (padding past the
+    step's tokens)."""
+    if stream is not None:
         with _on(stream):
-            i32 = lambda n: torch.empty(n, dtype=torch.int32, device=dev)  # noqa: E731
-            i64 = lambda n: torch.empty(n, dtype=torch.int64, device=dev)  # noqa: E731
-            out = PageMaps(i32(B + 1), i32(B), i64(max_tokens), i32(max_tokens), i32(max_tokens), i32(max_tokens),
-                           i64(max_tokens), i32(1))
-    else:
-        for t, name, dt, n in ((out.query_start, "query_start", torch.int32, B + 1),
-                               (out.seq_lens, "seq_lens", torch.int32, B),
-                               (out.slots, "slots", torch.int64, max_tokens),
-                               (out.positions, "positions", torch.int32, max_tokens),
-                               (out.token_request, "token_request", torch.int32, max_tokens),
-                               (out.visible_cols, "visible_cols", torch.int32, max_tokens),
-                               (out.column_slots, "column_slots", torch.int64, max_tokens),
-                               (out.pages_used, "pages_used", torch.int32, 1)):
-            _vec(t, name, dt, n)
-    desc = _abi.PageMapsDesc(B, int(page_tokens), block_table.shape[1], int(ratio), 1 if partial_cols else 0, 0,
-                             _strides(block_table)[0], free_pages.numel(), int(max_tokens))
-    _abi.build_page_maps(desc, context_lens, new_lens, free_pages, block_table, *out, stream=stream)
-    return out
-
-
-def _kv_desc(k_cache: torch.Tensor, v_cache: torch.Tensor) -> _abi.KvDesc:
-    _need(k_cache.dtype in _HALF and v_cache.dtype == k_cache.dtype, "the caches must both be bf16 or both fp16")
-    _need(k_cache.dim() == 4 and v_cache.shape == k_cache.shape,
-          "the caches must be [num_pages, page_tokens, num_kv_heads, head_dim], values like keys")
-    _need(k_cache.stride(3) == 1 and v_cache.stride(3) == 1, "the caches' last dimension must be contiguous")
-    e = 2
-    pages, pt, h, d = k_cache.shape
-    return _abi.KvDesc(_HALF[k_cache.dtype], pages, pt, h, d, 0, *(s * e for s in _strides(k_cache)[:3]),
-                       *(s * e for s in _strides(v_cache)[:3]))
+            return build_page_maps(context_lens, new_lens, free_pages, block_table, page_tokens=page_tokens,
+                                   max_tokens=max_tokens, ratio=ratio, partial_cols=partial_cols, out=out)
+    st, *maps = _qsa_torch.build_page_maps(context_lens, new_lens, free_pages, block_table, page_tokens, max_tokens,
+                                           ratio, partial_cols, out)
+    if st:
+        _abi._check(st)
+    return PageMaps._make(maps) if out is None else out
 
 
 def store_paged_kv(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
@@ -232,15 +190,12 @@ def store_paged_kv(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cach
     projection go as they are; slots: int64 [T], rows with a slot outside the
     cache are skipped; caches: [num_pages, page_tokens, num_kv_heads, head_dim]
     of any strides (permute a head-major cache into this order)."""
-    desc = _kv_desc(k_cache, v_cache)
-    T = slots.numel()
-    _vec(slots, "slots", torch.int64, -1)
-    for t, name in ((k, "k"), (v, "v")):
-        _need(t.dtype == k_cache.dtype and t.dim() == 3 and tuple(t.shape) == (T, *k_cache.shape[2:]) and
-              t.stride(2) == 1, f"{name} must be [T, num_kv_heads, head_dim] in the cache's type, last dimension "
-              f"contiguous")
-    ks, vs = _strides(k), _strides(v)
-    _abi.store_paged_kv(desc, k, ks[0] * 2, ks[1] * 2, v, vs[0] * 2, vs[1] * 2, slots, T, k_cache, v_cache, stream)
+    if stream is not None:
+        with _on(stream):
+            return store_paged_kv(k, v, slots, k_cache, v_cache)
+    st = _qsa_torch.store_paged_kv(k, v, slots, k_cache, v_cache)
+    if st:
+        _abi._check(st)
 
 
 def store_index_keys(keys: torch.Tensor, slots: torch.Tensor, kv_cache: torch.Tensor, *, page_cols: int,
@@ -250,39 +205,13 @@ def store_index_keys(keys: torch.Tensor, slots: torch.Tensor, kv_cache: torch.Te
     int64 [T] column slots (build_page_maps' column_slots), rows outside the
     cache skipped; kv_cache, page_cols, kv_dtype and scale_offset as in
     paged_mqa_logits (fp8: keys are quantised with one scale each)."""
-    T = slots.numel()
-    _vec(slots, "slots", torch.int64, -1)
-    _need(keys.dtype == torch.bfloat16 and keys.dim() == 2 and keys.shape[0] == T and keys.stride(1) == 1,
-          "keys must be bf16 [T, head_dim] with contiguous rows")
-    stride = kv_cache.stride(0) * kv_cache.element_size()
-    fp8 = kv_dtype == _abi.KV_FP8_E4M3
-    _need(not fp8 or scale_offset >= 0, "fp8 keys need the scale offset inside a block")
-    _need(fp8 or kv_cache.dtype == torch.bfloat16, "a bf16 index cache must be a bf16 tensor")
-    used = scale_offset + 4 * page_cols if fp8 else page_cols * 256
-    _need(kv_cache[0].is_contiguous() and kv_cache[0].numel() * kv_cache.element_size() >= used if len(kv_cache)
-          else False, "a page of kv_cache must be contiguous and hold page_cols keys (and scales)")
-    desc = _abi.IndexCacheDesc(kv_dtype, kv_cache.shape[0], int(page_cols), keys.shape[1], stride, stride if fp8 else 0)
-    _abi.store_index_keys(desc, keys, _strides(keys)[0] * 2, slots, T, kv_cache,
-                          kv_cache.data_ptr() + scale_offset if fp8 else None, stream)
-
-
-_attn_workspaces: dict = {}
-
-
-def _attention_workspace(nbytes: int, device: torch.device, stream) -> torch.Tensor:
-    with _on(stream):
-        def fresh():
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-            ws[:_abi.ATTN_COUNTER_BYTES].zero_()
-            return ws
-
-        if torch.cuda.is_current_stream_capturing():
-            return fresh()  # belongs to the graph: replays must not meet eager calls in it
-        key = (torch.cuda.current_device(), torch.cuda.current_stream().cuda_stream)
-        ws = _attn_workspaces.get(key)
-        if ws is None or ws.numel() < nbytes:
-            ws = _attn_workspaces[key] = fresh()
-        return ws
+    if stream is not None:
+        with _on(stream):
+            return store_index_keys(keys, slots, kv_cache, page_cols=page_cols, kv_dtype=kv_dtype,
+                                    scale_offset=scale_offset)
+    st = _qsa_torch.store_index_keys(keys, slots, kv_cache, page_cols, kv_dtype, scale_offset)
+    if st:
+        _abi._check(st)
 
 
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -306,36 +235,13 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     Without a workspace, one is kept for each stream that calls; a call under
     graph capture gets its own, cleared again by every replay (a given
     workspace, zeroed once, spares that)."""
-    _need(q.dim() == 3 and q.dtype == k_cache.dtype and q.stride(2) == 1,
-          "q must be [T, num_q_heads, head_dim] in the caches' type, last dimension contiguous")
-    kv = _kv_desc(k_cache, v_cache)
-    T, H, D = q.shape
-    _need(D == kv.head_dim, "q and the caches differ in head_dim")
-    _table(block_table)
-    B = block_table.shape[0]
-    _vec(query_start, "query_start", torch.int32, B + 1)
-    _vec(seq_lens, "seq_lens", torch.int32, B)
-    k = 0
-    if selected is not None:
-        _vec(selected, "selected", torch.int32, T, -1)
-        k = selected.shape[1]
-        _need(k > 0, "selected lists no columns")
-    with _on(stream):
-        if out is None:
-            out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
-        if lse is None and return_lse:
-            lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    _need(out.shape == q.shape and out.dtype == q.dtype and out.stride(2) == 1,
-          "out must have q's shape and type, last dimension contiguous")
-    if lse is not None:
-        _vec(lse, "lse", torch.float32, T, H)
-    e, qs, os = 2, _strides(q), _strides(out)
-    desc = _abi.AttnDesc(kv, B, H, block_table.shape[1], int(max_new), k, int(ratio), int(local_tokens), int(form), T,
-                         _strides(block_table)[0], qs[0] * e, qs[1] * e, os[0] * e, os[1] * e,
-                         D ** -0.5 if scale is None else float(scale), 0)
-    nbytes = _abi.paged_attention_workspace_bytes(desc)
-    if workspace is None:
-        workspace = _attention_workspace(nbytes, q.device, stream)
-    _abi.paged_attention(desc, q, k_cache, v_cache, block_table, query_start, seq_lens, selected, out, lse, workspace,
-                         workspace.numel() * workspace.element_size(), stream)
+    if stream is not None:
+        with _on(stream):
+            return paged_attention(q, k_cache, v_cache, block_table, query_start, seq_lens, scale=scale,
+                                   max_new=max_new, selected=selected, ratio=ratio, local_tokens=local_tokens,
+                                   form=form, out=out, lse=lse, return_lse=return_lse, workspace=workspace)
+    st, out, lse = _qsa_torch.paged_attention(q, k_cache, v_cache, block_table, query_start, seq_lens, scale, max_new,
+                                              selected, ratio, local_tokens, form, out, lse, return_lse, workspace)
+    if st:
+        _abi._check(st)
     return out if lse is None else (out, lse)

@@ -19,6 +19,7 @@ torch = pytest.importorskip("torch")
 
 import sparse_attention_indexer_02_gb300 as qsa  # noqa: E402
 from sparse_attention_indexer_02_gb300 import _abi, torch_api  # noqa: E402
+from sparse_attention_indexer_02_gb300 import build as qbuild  # noqa: E402
 
 gpu = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
@@ -26,6 +27,7 @@ DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
 
 @pytest.fixture(scope="module")
 def lib():
+    qbuild.build()
     return qsa.load_library()
 
 
@@ -196,7 +198,7 @@ def test_torch_api_refuses_wrong_tensors(lib):
     for name, t in (("q", q.half()), ("q", q[:, :, :64]), ("v_cache", kc.half()), ("v_cache", kc[:, :8]),
                     ("k_cache", kc.float()), ("block_table", i32(2, 4).long()), ("block_table", i32(4, 2).T),
                     ("query_start", i32(2)), ("seq_lens", i32(2).long()), ("seq_lens", i32(3))):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="must|differ"):
             torch_api.paged_attention(**{**ok, name: t})
     for kw in (dict(selected=i32(2, 4)), dict(selected=i32(3, 0)), dict(out=q.half()), dict(lse=torch.zeros(3, 4))):
         with pytest.raises(ValueError):
@@ -219,6 +221,27 @@ def test_torch_api_refuses_wrong_tensors(lib):
                  (i32(2).long(), i32(2), i32(4), i32(2, 4))):
         with pytest.raises(ValueError):
             torch_api.build_page_maps(*args, page_tokens=16, max_tokens=4)
+
+
+def test_torch_api_refuses_host_tensors(lib):
+    """Tensors that fit in every other way, but lie in host memory."""
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    kc = torch.zeros((4, 16, 2, 128), dtype=torch.bfloat16)
+    kv, slots = torch.zeros((3, 2, 128), dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int64)
+    for call in (lambda: torch_api.paged_attention(torch.zeros((3, 8, 128), dtype=torch.bfloat16), kc, kc, i32(2, 4),
+                                                   i32(3), i32(2)),
+                 lambda: torch_api.store_paged_kv(kv, kv, slots, kc, kc),
+                 lambda: torch_api.store_index_keys(torch.zeros((3, 128), dtype=torch.bfloat16), slots,
+                                                    torch.zeros((4, 16, 128), dtype=torch.bfloat16), page_cols=16),
+                 lambda: torch_api.build_page_maps(i32(2), i32(2), i32(4), i32(2, 4), page_tokens=16, max_tokens=4)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+    for call in (lambda: torch_api.store_paged_kv(None, kv, slots, kc, kc),
+                 lambda: torch_api.build_page_maps(i32(2), i32(2), i32(4), i32(2, 4), page_tokens="16", max_tokens=4),
+                 lambda: torch_api.build_page_maps(i32(2), i32(2), i32(4), i32(2, 4), page_tokens=1 << 40,
+                                                   max_tokens=4)):
+        with pytest.raises((ValueError, TypeError)):
+            call()
 
 
 # ---------------------------------------------------------------------------
