@@ -176,6 +176,7 @@ struct Walker {
       it.i0 += p.tpi;
     }
   }
+  __device__ __forceinline__ Walker(const AttnParams& p_, const Item& at) : p(p_), it(at), r(request_of(p_, at.b)) {}
   __device__ __forceinline__ void set() {
     it.n = min(p.tpi, r.n - it.i0);
     it.row0 = r.first + it.i0;

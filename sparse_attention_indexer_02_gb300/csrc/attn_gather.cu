@@ -13,13 +13,15 @@
 // the kernel is a stream first: every warp works alone on 16 keys at a time
 // (warp w of the CTA's 8 on keys 16 w .. 16 w + 15 of each 128-key unit) with
 // a ring of kStages 16-key stages of its own, and no barrier stands between
-// the warps until an item ends.  A stage is filled by 32 bulk copies, one a
-// lane: lanes 0-15 a key row each, lanes 16-31 a value row each.  Rows may lie
-// anywhere, so pages of any size, any cache strides and selected columns are
-// one path, and only rows that are seen are copied; the others are zeroed, so
-// that nothing a cache holds elsewhere can enter a product.  Rows are 16 bytes
-// apart more than their length, which keeps the matrix loads free of bank
-// conflicts.  192 KB of copies in flight on each SM cover the latency.
+// the warps until an item ends; even then the next item's first stages are on
+// their way.  A stage is filled by 16-byte asynchronous copies, half a warp a
+// row, from row addresses that each lane works out for one row and the warp
+// passes round by shuffles.  Rows may lie anywhere, so pages of any size, any
+// cache strides and selected columns are one path; rows that are not seen are
+// filled with zeros by the same instruction (source size 0), so that nothing a
+// cache holds elsewhere can enter a product.  Rows are 16 bytes apart more than
+// their length, which keeps the matrix loads free of bank conflicts.  192 KB
+// of copies in flight on each SM cover the latency.
 //
 // The products are mma.sync (m16n8k16): with at most 32 query rows a tcgen05
 // tile of 128 rows would be three quarters padding, and the stream leaves the
@@ -55,11 +57,23 @@ struct Layout {
   static constexpr int kRows = 16 * MT;
   static constexpr int q = kWarps * Geo<D>::kWarpBytes;
   static constexpr int ml = q + kRows * Geo<D>::kRow;          // [warp][row] of (m, l)
-  static constexpr int bars = ml + kWarps * kRows * 8;         // [warp][stage]
-  static constexpr int masks = bars + kWarps * kStages * 8;    // [warp][stage]
-  static constexpr int total = masks + kWarps * kStages * 4;
-  static_assert(kRows * Geo<D>::kMergeRow * 4 <= Geo<D>::kWarpBytes, "a warp's o fits its stages");
-  static_assert(total <= 226 * 1024, "shared memory");
+  static constexpr int total = ml + kWarps * kRows * 8;
+  static_assert(16 * Geo<D>::kMergeRow * 4 <= Geo<D>::kStage, "16 rows of a warp's o fit a stage");
+  static_assert(MT < kStages, "a stage for the next item while the warps join");
+  static_assert(total <= 225 * 1024, "shared memory");
+};
+
+// What the warps need of an item, in shared memory.
+struct ItemSh {
+  int32_t ua, uz;          // its units in this CTA's share
+  int32_t row0, n, pos0, keys;
+  int32_t gs, head0;       // query heads of the virtual head, the first of them
+  int32_t local0;          // SEL: first of the last tokens
+  int32_t c0, c1;          // the CTAs it lies in
+  int32_t live;            // it exists
+  int64_t k_off, v_off;    // of its key/value head in the caches
+  const int32_t* table;
+  const int32_t* sel;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -88,10 +102,17 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void bulk_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-               : "memory");
+// 16 bytes to shared memory; zeros, nothing read, when `bytes` is 0.
+__device__ __forceinline__ void copy16(uint32_t dst, uint64_t src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until all but the `ahead` youngest groups have landed (0 .. kStages - 1).
+__device__ __forceinline__ void copies_wait(uint32_t ahead) {
+  static_assert(kStages == 3, "one case a stage");
+  if (ahead >= 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (ahead == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // An unfinished part: o [kRows][D] floats, then (m, l) of each row.
@@ -100,35 +121,79 @@ constexpr int64_t part_floats() {
   return 16 * MT * (D + 2);
 }
 
+// The item of unit u of a selected call: one token row of one virtual head.
+__device__ __forceinline__ Item selected_item(const AttnParams& p, int64_t u, int32_t units, int32_t from_b) {
+  Item it;
+  const int64_t i = u / units;
+  const int32_t t = (int32_t)(i / p.hv);
+  it.hv = (int32_t)(i - (int64_t)t * p.hv);
+  it.s0 = i * units;
+  it.s1 = it.s0 + units;
+  it.row0 = t;
+  it.n = 1;
+  it.i0 = 0;
+  int lo = from_b, hi = p.num_requests;  // the last request that starts at or before t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.query_start[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  it.b = lo;
+  const Request r = request_of(p, lo);
+  it.pos0 = t < r.first + r.n ? r.pos0 + (t - r.first) : -1;
+  it.keys = min(max(it.pos0 + 1, 0), p.capacity);
+  return it;
+}
+
+template <bool SEL>
+__device__ __forceinline__ void publish(const AttnParams& p, const Schedule& s, const Item& it, ItemSh* o) {
+  const int kvh = it.hv / p.splits;
+  const int sub0 = (it.hv - kvh * p.splits) * p.sub;
+  o->ua = (int)(max(s.u0, it.s0) - it.s0);
+  o->uz = (int)(min(s.u1, it.s1) - it.s0);
+  o->row0 = it.row0;
+  o->n = it.n;
+  o->pos0 = it.pos0;
+  o->keys = it.keys;
+  o->gs = min(p.sub, p.group - sub0);
+  o->head0 = kvh * p.group + sub0;
+  o->local0 = it.pos0 + 1 - p.local_tokens;
+  const int c = (int)blockIdx.x;
+  o->c0 = it.s0 >= s.u0 ? c : s.owner(it.s0);
+  o->c1 = it.s1 <= s.u1 ? c : s.owner(it.s1 - 1);
+  o->live = 1;
+  o->k_off = (int64_t)kvh * p.k_head_stride;
+  o->v_off = (int64_t)kvh * p.v_head_stride;
+  o->table = p.block_table + (int64_t)it.b * p.table_stride;
+  o->sel = SEL ? p.selected + (int64_t)it.row0 * p.num_selected : nullptr;
+}
+
 template <bool F16, int D, int MT, bool SEL>
 __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p) {
   using G = Geo<D>;
   using L = Layout<D, MT>;
   constexpr int kRows = 16 * MT;
+  constexpr int kChunks = D / 8;            // 16-byte chunks of a row
+  constexpr int kRpi = 32 / kChunks;        // rows a copy instruction of the warp
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ SchedShared sched_sh;
-  __shared__ int abort_sh;
+  __shared__ Item walk_item;                // thread 0's place in the list
+  __shared__ ItemSh items[2];               // this item and the next, by turns
+  __shared__ uint32_t masks_sh[kWarps][kStages];  // SEL: the rows of a stage that are seen
   __shared__ int last_sh;
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::bars) + warp * kStages;
-  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + L::masks) + warp * kStages;
   float2* ml = reinterpret_cast<float2*>(smem + L::ml);
   uint8_t* ring = smem + warp * G::kWarpBytes;
   const uint32_t ring_u32 = ptx::smem_u32(ring);
-  volatile int* abort_flag = &abort_sh;
 
-  if (lane == 0)
-    for (int s = 0; s < kStages; ++s) ptx::mbar_init(&bars[s], 1);
-  if (tid == 0) abort_sh = 0;
-  ptx::fence_mbar_init();
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
 
   // ---- the CTA's share of the units
   const int32_t list_len = SEL ? p.num_selected * p.ratio + p.local_tokens : 0;
+  const int32_t sel_end = SEL ? p.num_selected * p.ratio : 0;
   const int32_t sel_units = SEL ? units_of(list_len) : 0;
   Schedule s;
-  int32_t sel_b = 0;
   if (SEL) {
     const int64_t rows = min(max(p.query_start[p.num_requests], 0), p.num_tokens);
     s.total = rows * p.hv * sel_units;
@@ -137,131 +202,133 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
     const int c = (int)blockIdx.x;
     s.u0 = c < s.ge ? s.share(c) : s.total;
     s.u1 = c < s.ge ? s.share(c + 1) : s.total;
-    __syncthreads();
   } else {
     s = make_schedule<kNT>(p, sched_sh);
   }
   if (s.u0 >= s.u1) return;
-
-  uint32_t issued = 0, used = 0;  // stages filled and consumed by this warp
-  bool ok = true;
-  const int r16 = lane & 15;
-  const bool is_v = lane >= 16;
-  const uint8_t* cache = is_v ? p.v : p.k;
-  const int64_t page_stride = is_v ? p.v_page_stride : p.k_page_stride;
-  const int64_t token_stride = is_v ? p.v_token_stride : p.k_token_stride;
-  const int64_t head_stride = is_v ? p.v_head_stride : p.k_head_stride;
-
-  Item it;
-  auto sel_item = [&](int64_t u) {  // SEL: the item of unit u (one token row, one head)
-    const int64_t i = u / sel_units;
-    const int32_t t = (int32_t)(i / p.hv);
-    it.hv = (int32_t)(i - (int64_t)t * p.hv);
-    it.s0 = i * sel_units;
-    it.s1 = it.s0 + sel_units;
-    it.row0 = t;
-    it.n = 1;
-    int lo = sel_b, hi = p.num_requests;  // the last request that starts at or before t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.query_start[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    sel_b = it.b = lo;
-    const Request r = request_of(p, lo);
-    it.pos0 = r.pos0 + (t - r.first);
-    if (t >= r.first + r.n) it.pos0 = -1;
-    it.keys = min(max(it.pos0 + 1, 0), p.capacity);
-  };
-  Walker* walk = nullptr;
-  alignas(Walker) unsigned char walk_mem[sizeof(Walker)];
-  if (SEL) {
-    sel_item(s.u0);
-  } else {
-    walk = new (walk_mem) Walker(p, sched_sh, s.u0);
-    it = walk->it;
+  if (tid == 0) {
+    walk_item = SEL ? selected_item(p, s.u0, sel_units, 0) : Walker(p, sched_sh, s.u0).it;
+    publish<SEL>(p, s, walk_item, &items[0]);
   }
+  __syncthreads();
 
-  for (;;) {
-    const int64_t a = max(s.u0, it.s0), z = min(s.u1, it.s1);
-    const int ua = (int)(a - it.s0), uz = (int)(z - it.s0);
-    const int kvh = it.hv / p.splits;
-    const int sub0 = (it.hv - kvh * p.splits) * p.sub;
-    const int gs = min(p.sub, p.group - sub0);  // query heads of this virtual head
+  // ---- the copy side: (slot, j) is the next slice to copy, slice j of items[slot]
+  uint32_t issued = 0, used = 0;  // stages filled and consumed by this warp
+  const int r16 = lane & 15;
+  int slot = 0, ij = items[0].ua;
+  int32_t tok1, page1, col2 = 0;  // its token and page, loaded ahead; SEL: the column after it
+  auto sel_entry = [&](int j) -> int32_t {  // SEL: the column listed for the lane's place, -1 none
+    const int32_t at = j * kUnit + warp * kSlice + r16;
+    return j < items[slot].uz && at < sel_end ? __ldg(items[slot].sel + at / p.ratio) : -1;
+  };
+  auto token_of = [&](int j, int32_t col) -> int32_t {  // the lane's token, -1 none
+    const int32_t at = j * kUnit + warp * kSlice + r16;
+    const ItemSh& it = items[slot];
+    if (j >= it.uz) return -1;
+    if (!SEL) return at < it.keys ? at : -1;
+    int64_t t;
+    if (at < sel_end) {
+      t = (int64_t)col * p.ratio + at % p.ratio;
+      if (col < 0 || t >= it.local0) return -1;
+    } else {
+      t = (int64_t)it.local0 + (at - sel_end);
+      if (t < 0 || at >= list_len) return -1;
+    }
+    return t < it.keys ? (int32_t)t : -1;
+  };
+  auto page_of = [&](int32_t tok) -> int32_t {
+    if (tok < 0) return 0;
+    return __ldg(items[slot].table + (p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_tokens));
+  };
+  auto enter = [&]() {  // at the first slice of items[slot]
+    ij = items[slot].ua;
+    tok1 = token_of(ij, SEL ? sel_entry(ij) : 0);
+    page1 = page_of(tok1);
+    if (SEL) col2 = sel_entry(ij + 1);
+  };
+  enter();
+  auto issue = [&]() {  // copies the next slice into the next stage
+    const uint32_t st = ring_u32 + (issued % kStages) * G::kStage;
+    const uint32_t vm = __ballot_sync(0xffffffffu, tok1 >= 0) & 0xFFFFu;
+    const int32_t pg = min(max(page1, 0), p.num_pages - 1);
+    const int32_t tk = max(tok1, 0);
+    const int32_t off = p.page_shift >= 0 ? tk & (p.page_tokens - 1) : tk % p.page_tokens;
+    const ItemSh& it = items[slot];
+    const uint64_t ka = reinterpret_cast<uint64_t>(p.k) + (uint64_t)(it.k_off + (int64_t)pg * p.k_page_stride +
+                                                                     (int64_t)off * p.k_token_stride);
+    const uint64_t va = reinterpret_cast<uint64_t>(p.v) + (uint64_t)(it.v_off + (int64_t)pg * p.v_page_stride +
+                                                                     (int64_t)off * p.v_token_stride);
+    const int chunk = lane % kChunks;
+#pragma unroll
+    for (int i = 0; i < kSlice / kRpi; ++i) {
+      const int row = i * kRpi + lane / kChunks;
+      const uint64_t ks = __shfl_sync(0xffffffffu, ka, row), vs = __shfl_sync(0xffffffffu, va, row);
+      const uint32_t bytes = (vm >> row) & 1u ? 16u : 0u;
+      const uint32_t dst = st + row * G::kRow + chunk * 16;
+      copy16(dst, ks + chunk * 16, bytes);
+      copy16(dst + kSlice * G::kRow, vs + chunk * 16, bytes);
+    }
+    copies_commit();
+    if (SEL && lane == 0) masks_sh[warp][issued % kStages] = vm;
+    ++issued;
+    ++ij;
+    tok1 = token_of(ij, col2);
+    page1 = page_of(tok1);
+    if (SEL) col2 = sel_entry(ij + 1);
+  };
+
+  // `rem` slices of the current item (slot cur) are not consumed yet.  The next
+  // item's may take kStages - MT stages: the warps join in the others.
+  auto try_issue = [&](int cur, int rem) -> bool {
+    if (issued - used >= kStages) return false;
+    if (slot == cur) {
+      if (ij < items[cur].uz) {
+        issue();
+        return true;
+      }
+      if (!items[cur ^ 1].live) return false;
+      slot = cur ^ 1;
+      enter();
+    }
+    if (ij >= items[slot].uz || (int)(issued - used) - rem >= kStages - MT) return false;
+    issue();
+    return true;
+  };
+
+  for (int k = 0;; ++k) {
+    const int cur = k & 1;
+    const ItemSh& it = items[cur];
+    const int ua = it.ua, uz = it.uz, gs = it.gs, head0 = it.head0, row0 = it.row0;
     const int live = it.n * gs;
-    const int head0 = kvh * p.group + sub0;
 
-    // ---- q: rows (token, head) into shared memory, the padding rows zero
-    for (int i = tid; i < kRows * (D / 8); i += kNT) {
-      const int r = i / (D / 8), c = i - r * (D / 8);
+    // ---- the next item; q: rows (token, head) into shared memory, the padding rows zero
+    if (tid == 0) {
+      if (walk_item.s1 < s.u1) {
+        if (SEL) {
+          walk_item = selected_item(p, walk_item.s1, sel_units, walk_item.b);
+        } else {
+          Walker w(p, walk_item);
+          w.next();
+          walk_item = w.it;
+        }
+        publish<SEL>(p, s, walk_item, &items[cur ^ 1]);
+      } else {
+        items[cur ^ 1].live = 0;
+      }
+    }
+    for (int i = tid; i < kRows * kChunks; i += kNT) {
+      const int r = i / kChunks, c = i - r * kChunks;
       uint4 w = make_uint4(0, 0, 0, 0);
       if (r < live) {
         const int tk = r / gs, g = r - tk * gs;
-        w = *reinterpret_cast<const uint4*>(p.q + (int64_t)(it.row0 + tk) * p.q_token_stride +
+        w = *reinterpret_cast<const uint4*>(p.q + (int64_t)(row0 + tk) * p.q_token_stride +
                                             (int64_t)(head0 + g) * p.q_head_stride + c * 16);
       }
       *reinterpret_cast<uint4*>(smem + L::q + r * G::kRow + c * 16) = w;
     }
-
-    // ---- key list: the token at place j * 128 + warp * 16 + r16 of unit j
-    const uint8_t* base = cache + (int64_t)kvh * head_stride;
-    const int32_t* table = p.block_table + (int64_t)it.b * p.table_stride;
-    const int32_t* sel = SEL ? p.selected + (int64_t)it.row0 * p.num_selected : nullptr;
-    const int32_t sel_end = SEL ? p.num_selected * p.ratio : 0;
-    const int32_t local0 = SEL ? it.pos0 + 1 - p.local_tokens : 0;  // first of the last tokens
-    auto sel_entry = [&](int j) -> int32_t {  // SEL: the column listed for the lane's place, -1 none
-      const int32_t at = j * kUnit + warp * kSlice + r16;
-      return j < uz && at < sel_end ? __ldg(sel + at / p.ratio) : -1;
-    };
-    auto token_of = [&](int j, int32_t col) -> int32_t {  // the lane's token, -1 none
-      const int32_t at = j * kUnit + warp * kSlice + r16;
-      if (j >= uz) return -1;
-      if (!SEL) return at < it.keys ? at : -1;
-      int64_t t;
-      if (at < sel_end) {
-        t = (int64_t)col * p.ratio + at % p.ratio;
-        if (col < 0 || t >= local0) return -1;
-      } else {
-        t = (int64_t)local0 + (at - sel_end);
-        if (t < 0 || at >= list_len) return -1;
-      }
-      return t < it.keys ? (int32_t)t : -1;
-    };
-    auto page_of = [&](int32_t tok) -> int32_t {
-      if (tok < 0) return 0;
-      const int32_t pg = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_tokens;
-      return __ldg(table + pg);
-    };
-    // what the next stage needs, loaded one stage (columns: two) ahead
-    int32_t col2 = SEL ? sel_entry(ua + 1) : 0;
-    int32_t tok1 = token_of(ua, SEL ? sel_entry(ua) : 0);
-    int32_t page1 = page_of(tok1);
-    auto issue = [&](int j) {  // fills the next stage with unit j's slice
-      const int st = issued % kStages;
-      const bool valid = tok1 >= 0;
-      const uint32_t vm = __ballot_sync(0xffffffffu, valid);
-      const uint32_t dst = ring_u32 + st * G::kStage + lane * G::kRow;
-      if (lane == 0) {
-        masks[st] = vm & 0xFFFFu;
-        ptx::mbar_arrive_expect_tx(&bars[st], (uint32_t)__popc(vm) * 2 * D);
-      }
-      __syncwarp();
-      if (valid) {
-        const int32_t pg = min(max(page1, 0), p.num_pages - 1);
-        const int32_t off = p.page_shift >= 0 ? tok1 & (p.page_tokens - 1) : tok1 % p.page_tokens;
-        bulk_row(dst, base + (int64_t)pg * page_stride + (int64_t)off * token_stride, 2 * D, ptx::smem_u32(&bars[st]));
-      } else if (vm != 0) {
-        for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<uint4*>(ring + st * G::kStage + lane * G::kRow + c * 16) = make_uint4(0, 0, 0, 0);
-        ptx::fence_proxy_async_smem();  // before a later copy into the row
-      }
-      ++issued;
-      tok1 = token_of(j + 1, col2);
-      page1 = page_of(tok1);
-      if (SEL) col2 = sel_entry(j + 2);
-    };
-    for (int i = 0; i < kStages && ua + i < uz; ++i) issue(ua + i);
-    __syncthreads();  // q
+    __syncthreads();
+    while (try_issue(cur, uz - ua)) {
+    }
 
     uint32_t qf[MT == 1 ? D / 16 : 1][4];
     const uint32_t q_addr =
@@ -290,12 +357,12 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
     }
 
     for (int j = ua; j < uz; ++j) {
-      const int st = used % kStages;
-      if (ok) ok = __all_sync(0xffffffffu, wait_phase(&bars[st], (used / kStages) & 1u, abort_flag, p.fault));
-      ++used;
-      const uint32_t vm = masks[st];
-      if (ok && vm != 0) {
-        const uint32_t kb = ring_u32 + st * G::kStage;
+      copies_wait(issued - used - 1);
+      __syncwarp();
+      const int32_t key0 = j * kUnit + warp * kSlice;
+      const uint32_t vm = SEL ? masks_sh[warp][used % kStages] : 0u;
+      if (SEL ? vm != 0 : key0 < it.keys) {
+        const uint32_t kb = ring_u32 + (used % kStages) * G::kStage;
         float x[MT][2][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -320,7 +387,6 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
             mma16816<F16>(x[mt][1], aq, bk[2], bk[3]);
           }
         }
-        const int32_t key0 = j * kUnit + warp * kSlice;
         if (SEL ? vm != 0xFFFFu : key0 + kSlice > all_see) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
@@ -376,42 +442,35 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
         }
       }
       __syncwarp();
-      if (j + kStages < uz && ok) issue(j + kStages);
-    }
-    if (!ok) {  // gave up on a copy: let the others of this warp land before the memory is reused
-      for (; used < issued; ++used) {
-        const long long t0 = clock64();
-        while (!ptx::mbar_try_wait(&bars[used % kStages], (used / kStages) & 1u) && clock64() - t0 < kSpin) {
-        }
-      }
-      used = issued;
+      ++used;
+      try_issue(cur, uz - 1 - j);
     }
 
-    // ---- join the warps
+    // ---- join the warps, in the stages that hold nothing for the next item
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+      uint8_t* stage = ring + ((used + kStages - 1 - mt) % kStages) * G::kStage;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float t = l[mt][h];
         t += __shfl_xor_sync(0xffffffffu, t, 1);
         t += __shfl_xor_sync(0xffffffffu, t, 2);
-        const int r = mt * 16 + h * 8 + (lane >> 2);
-        if ((lane & 3) == 0) ml[warp * kRows + r] = make_float2(m[mt][h], t);
-        float* dst = reinterpret_cast<float*>(ring) + r * G::kMergeRow + (lane & 3) * 2;
+        const int r = h * 8 + (lane >> 2);
+        if ((lane & 3) == 0) ml[warp * kRows + mt * 16 + r] = make_float2(m[mt][h], t);
+        float* dst = reinterpret_cast<float*>(stage) + r * G::kMergeRow + (lane & 3) * 2;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
           *reinterpret_cast<float2*>(dst + i * 8) = make_float2(o[mt][i][2 * h], o[mt][i][2 * h + 1]);
       }
+    }
     __syncthreads();
 
-    const int c = (int)blockIdx.x;
-    const int c0 = it.s0 >= s.u0 ? c : s.owner(it.s0);
-    const int c1 = it.s1 <= s.u1 ? c : s.owner(it.s1 - 1);
+    const int c = (int)blockIdx.x, c0 = it.c0, c1 = it.c1;
     const bool split = c0 != c1;
     float* part = p.parts + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * part_floats<D, MT>();
     auto write_out = [&](int r, int d, float M, float Lsum, const float (&acc)[4]) {
       const int tk = r / gs, g = r - tk * gs;
-      const int64_t row = it.row0 + tk;
+      const int64_t row = row0 + tk;
       const float inv = Lsum > 0.0f ? 1.0f / Lsum : (Lsum == 0.0f ? 0.0f : Lsum);
       uint2 w = make_uint2(pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv));
       *reinterpret_cast<uint2*>(p.out + row * p.out_token_stride + (int64_t)(head0 + g) * p.out_head_stride + d * 2) = w;
@@ -429,7 +488,9 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
         const float2 e = ml[w * kRows + r];
         const float f = e.x == -INFINITY ? 0.0f : ex2(e.x - M);
         const float4 v = *reinterpret_cast<const float4*>(
-            reinterpret_cast<const float*>(smem + w * G::kWarpBytes) + r * G::kMergeRow + d);
+            reinterpret_cast<const float*>(smem + w * G::kWarpBytes +
+                                           ((used + kStages - 1 - (r >> 4)) % kStages) * G::kStage) +
+            (r & 15) * G::kMergeRow + d);
         Ls += e.y * f;
         acc[0] = fmaf(v.x, f, acc[0]);
         acc[1] = fmaf(v.y, f, acc[1]);
@@ -479,14 +540,7 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
         }
       }
     }
-    if (z == s.u1) break;
-    if (SEL) {
-      sel_item(it.s1);
-    } else {
-      walk->next();
-      it = walk->it;
-    }
-    ptx::fence_proxy_async_smem();  // the stages were written by plain stores
+    if (!items[cur ^ 1].live) break;
     __syncthreads();
   }
 }
