@@ -1,7 +1,7 @@
 // Parameters and the work schedule shared by the two forms of
 // qsa_paged_attention (attn_gather.cu, attn_tile.cu).
 //
-// Work is counted in units of 128 keys of one item; an item is a group of
+// Work is counted in units of `unit` keys (128, or 192) of one item; an item is a group of
 // query rows that share their keys: `tpi` consecutive new tokens of a request
 // times the query heads of a (virtual) key/value head.  The items of a call,
 // request by request, then head by head, then along the tokens, form one list
@@ -23,7 +23,6 @@
 namespace qsa {
 namespace attn {
 
-constexpr int kUnit = 128;      // keys a unit
 constexpr int kMaxGrid = 160;   // CTAs a launch, at most (GB300 has 152 SMs)
 static_assert(kMaxGrid * 4 == QSA_ATTN_COUNTER_BYTES, "one counter a CTA");
 constexpr float kLn2 = 0.6931471805599453f;
@@ -60,12 +59,14 @@ __device__ __forceinline__ int32_t keys_of(const AttnParams& p, const Request& r
   return min(max(r.pos0 + i1, 0), p.capacity);
 }
 
-__device__ __forceinline__ int32_t units_of(int32_t keys) { return max(1, (keys + kUnit - 1) / kUnit); }
+__device__ __forceinline__ int32_t units_of(const AttnParams& p, int32_t keys) {
+  return max(1, (keys + p.unit - 1) / p.unit);
+}
 
 // Units of one head of a request: the sum over its items.
 __device__ __forceinline__ int64_t head_units(const AttnParams& p, const Request& r) {
   int64_t u = 0;
-  for (int i = 0; i < r.n; i += p.tpi) u += units_of(keys_of(p, r, min(i + p.tpi, r.n)));
+  for (int i = 0; i < r.n; i += p.tpi) u += units_of(p, keys_of(p, r, min(i + p.tpi, r.n)));
   return u;
 }
 
@@ -165,7 +166,7 @@ struct Walker {
     it.i0 = 0;
     for (;;) {
       set();
-      const int32_t u = units_of(it.keys);
+      const int32_t u = units_of(p, it.keys);
       if (rem < u) {
         it.s0 = s;
         it.s1 = s + u;
@@ -196,7 +197,7 @@ struct Walker {
     }
     set();
     it.s0 = it.s1;
-    it.s1 += units_of(it.keys);
+    it.s1 += units_of(p, it.keys);
   }
 };
 

@@ -38,28 +38,39 @@ namespace qsa {
 namespace attn {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kNT = 32 * kWarps;
-constexpr int kStages = 3;
-constexpr int kSlice = kUnit / kWarps;  // keys a stage
-static_assert(kSlice == 16, "a stage is one k-step of the second product");
+constexpr int kSlice = 16;       // keys a stage: one k-step of the second product
+constexpr float kRaise = 8.0f;
 
-template <int D>
+// One 16-row tile: 12 warps with two stages each (168 registers a thread).  A
+// slice is a chain of dependent steps that a warp takes 2000 cycles and more
+// for, whatever the memory does, so three warps a scheduler pay more than a
+// third stage (MEASURED).  Two tiles hold
+// twice the accumulators, 8 warps' worth, and take three stages.
+template <int MT>
+struct Conf {
+  static constexpr int kWarps = MT == 1 ? 12 : 8;
+  static constexpr int kStages = MT == 1 ? 2 : 3;
+  static constexpr int kNT = 32 * kWarps;
+  static constexpr int kUnit = kWarps * kSlice;  // keys a unit of the schedule
+};
+
+template <int D, int MT>
 struct Geo {
   static constexpr int kRow = 2 * D + 16;                  // bytes from row to row
   static constexpr int kStage = 2 * kSlice * kRow;         // key rows, then value rows
-  static constexpr int kWarpBytes = kStages * kStage;
+  static constexpr int kWarpBytes = Conf<MT>::kStages * kStage;
   static constexpr int kMergeRow = D + 4;                  // floats from row to row of a warp's o
 };
 
 template <int D, int MT>
 struct Layout {
+  using G = Geo<D, MT>;
   static constexpr int kRows = 16 * MT;
-  static constexpr int q = kWarps * Geo<D>::kWarpBytes;
-  static constexpr int ml = q + kRows * Geo<D>::kRow;          // [warp][row] of (m, l)
-  static constexpr int total = ml + kWarps * kRows * 8;
-  static_assert(16 * Geo<D>::kMergeRow * 4 <= Geo<D>::kStage, "16 rows of a warp's o fit a stage");
-  static_assert(MT < kStages, "a stage for the next item while the warps join");
+  static constexpr int q = Conf<MT>::kWarps * G::kWarpBytes;
+  static constexpr int ml = q + kRows * G::kRow;               // [warp][row] of (m, l)
+  static constexpr int total = ml + Conf<MT>::kWarps * kRows * 8;
+  static_assert(16 * G::kMergeRow * 4 <= G::kStage, "16 rows of a warp's o fit a stage");
+  static_assert(MT < Conf<MT>::kStages, "a stage for the next item while the warps join");
   static_assert(total <= 225 * 1024, "shared memory");
 };
 
@@ -79,24 +90,22 @@ struct ItemSh {
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if (F16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -107,9 +116,8 @@ __device__ __forceinline__ void copy16(uint32_t dst, uint64_t src, uint32_t byte
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits until all but the `ahead` youngest groups have landed (0 .. kStages - 1).
+// Waits until all but the `ahead` youngest groups have landed (0, 1 or 2).
 __device__ __forceinline__ void copies_wait(uint32_t ahead) {
-  static_assert(kStages == 3, "one case a stage");
   if (ahead >= 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
   else if (ahead == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
   else asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -169,9 +177,10 @@ __device__ __forceinline__ void publish(const AttnParams& p, const Schedule& s, 
 }
 
 template <bool F16, int D, int MT, bool SEL>
-__global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p) {
-  using G = Geo<D>;
+__global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const AttnParams p) {
+  using G = Geo<D, MT>;
   using L = Layout<D, MT>;
+  constexpr int kWarps = Conf<MT>::kWarps, kStages = Conf<MT>::kStages, kNT = Conf<MT>::kNT, kUnit = Conf<MT>::kUnit;
   constexpr int kRows = 16 * MT;
   constexpr int kChunks = D / 8;            // 16-byte chunks of a row
   constexpr int kRpi = 32 / kChunks;        // rows a copy instruction of the warp
@@ -192,7 +201,7 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
   // ---- the CTA's share of the units
   const int32_t list_len = SEL ? p.num_selected * p.ratio + p.local_tokens : 0;
   const int32_t sel_end = SEL ? p.num_selected * p.ratio : 0;
-  const int32_t sel_units = SEL ? units_of(list_len) : 0;
+  const int32_t sel_units = SEL ? units_of(p, list_len) : 0;
   Schedule s;
   if (SEL) {
     const int64_t rows = min(max(p.query_start[p.num_requests], 0), p.num_tokens);
@@ -217,9 +226,10 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
   const int r16 = lane & 15;
   int slot = 0, ij = items[0].ua;
   int32_t tok1, page1, col2 = 0;  // its token and page, loaded ahead; SEL: the column after it
+  auto col_of = [&](int32_t at) -> int32_t { return p.ratio_shift >= 0 ? at >> p.ratio_shift : at / p.ratio; };
   auto sel_entry = [&](int j) -> int32_t {  // SEL: the column listed for the lane's place, -1 none
     const int32_t at = j * kUnit + warp * kSlice + r16;
-    return j < items[slot].uz && at < sel_end ? __ldg(items[slot].sel + at / p.ratio) : -1;
+    return j < items[slot].uz && at < sel_end ? __ldg(items[slot].sel + col_of(at)) : -1;
   };
   auto token_of = [&](int j, int32_t col) -> int32_t {  // the lane's token, -1 none
     const int32_t at = j * kUnit + warp * kSlice + r16;
@@ -228,7 +238,7 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
     if (!SEL) return at < it.keys ? at : -1;
     int64_t t;
     if (at < sel_end) {
-      t = (int64_t)col * p.ratio + at % p.ratio;
+      t = (int64_t)col * p.ratio + (at - col_of(at) * p.ratio);
       if (col < 0 || t >= it.local0) return -1;
     } else {
       t = (int64_t)it.local0 + (at - sel_end);
@@ -254,19 +264,33 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
     const int32_t tk = max(tok1, 0);
     const int32_t off = p.page_shift >= 0 ? tk & (p.page_tokens - 1) : tk % p.page_tokens;
     const ItemSh& it = items[slot];
-    const uint64_t ka = reinterpret_cast<uint64_t>(p.k) + (uint64_t)(it.k_off + (int64_t)pg * p.k_page_stride +
-                                                                     (int64_t)off * p.k_token_stride);
-    const uint64_t va = reinterpret_cast<uint64_t>(p.v) + (uint64_t)(it.v_off + (int64_t)pg * p.v_page_stride +
-                                                                     (int64_t)off * p.v_token_stride);
     const int chunk = lane % kChunks;
+    const int64_t ko = it.k_off + (int64_t)pg * p.k_page_stride + (int64_t)off * p.k_token_stride;
+    if (p.near_rows) {  // one 32-bit offset a row, in units of 16 bytes, for key and value
+      const uint32_t o16 = (uint32_t)(ko >> 4);
+      const uint8_t *kb = p.k + chunk * 16, *vb = p.v + chunk * 16;
 #pragma unroll
-    for (int i = 0; i < kSlice / kRpi; ++i) {
-      const int row = i * kRpi + lane / kChunks;
-      const uint64_t ks = __shfl_sync(0xffffffffu, ka, row), vs = __shfl_sync(0xffffffffu, va, row);
-      const uint32_t bytes = (vm >> row) & 1u ? 16u : 0u;
-      const uint32_t dst = st + row * G::kRow + chunk * 16;
-      copy16(dst, ks + chunk * 16, bytes);
-      copy16(dst + kSlice * G::kRow, vs + chunk * 16, bytes);
+      for (int i = 0; i < kSlice / kRpi; ++i) {
+        const int row = i * kRpi + lane / kChunks;
+        const uint64_t o = (uint64_t)__shfl_sync(0xffffffffu, o16, row) << 4;
+        const uint32_t bytes = (vm >> row) & 1u ? 16u : 0u;
+        const uint32_t dst = st + row * G::kRow + chunk * 16;
+        copy16(dst, reinterpret_cast<uint64_t>(kb) + o, bytes);
+        copy16(dst + kSlice * G::kRow, reinterpret_cast<uint64_t>(vb) + o, bytes);
+      }
+    } else {
+      const uint64_t ka = reinterpret_cast<uint64_t>(p.k) + (uint64_t)ko;
+      const uint64_t va = reinterpret_cast<uint64_t>(p.v) + (uint64_t)(it.v_off + (int64_t)pg * p.v_page_stride +
+                                                                       (int64_t)off * p.v_token_stride);
+#pragma unroll 1
+      for (int i = 0; i < kSlice / kRpi; ++i) {
+        const int row = i * kRpi + lane / kChunks;
+        const uint64_t ks = __shfl_sync(0xffffffffu, ka, row), vs = __shfl_sync(0xffffffffu, va, row);
+        const uint32_t bytes = (vm >> row) & 1u ? 16u : 0u;
+        const uint32_t dst = st + row * G::kRow + chunk * 16;
+        copy16(dst, ks + chunk * 16, bytes);
+        copy16(dst + kSlice * G::kRow, vs + chunk * 16, bytes);
+      }
     }
     copies_commit();
     if (SEL && lane == 0) masks_sh[warp][issued % kStages] = vm;
@@ -408,7 +432,9 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             mx *= p.scale_log2;
-            if (__any_sync(0xffffffffu, mx > m[mt][h])) {
+            // m is raised when a maximum passes it by more than 8 only: any m that keeps
+            // the exponentials in range gives the same quotient, and raising costs a pass over o
+            if (__any_sync(0xffffffffu, mx > m[mt][h] + kRaise || (m[mt][h] == -INFINITY && mx > m[mt][h]))) {
               const float mn = fmaxf(m[mt][h], mx);
               const float f = mn == -INFINITY ? 1.0f : ex2(m[mt][h] - mn);
               m[mt][h] = mn;
@@ -554,7 +580,7 @@ cudaError_t launch_t(const AttnParams& p, int device, int grid, cudaStream_t str
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
-  cfg.blockDim = dim3(kNT, 1, 1);
+  cfg.blockDim = dim3(Conf<MT>::kNT, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -599,7 +625,16 @@ cudaError_t launch_attn_gather(AttnParams p, const qsa_attn_desc& d, uint8_t* wo
     toks = d.max_new > 0 ? d.max_new : (d.num_tokens + d.num_requests - 1) / d.num_requests;
   const int mt = toks * p.sub <= 16 ? 1 : 2;
   p.tpi = p.num_selected > 0 ? 1 : 16 * mt / p.sub;
+  p.unit = mt == 1 ? Conf<1>::kUnit : Conf<2>::kUnit;
   p.min_units = 1;
+  p.ratio_shift = -1;
+  for (int sh = 0; sh < 31; ++sh)
+    if ((1 << sh) == p.ratio) p.ratio_shift = sh;
+  const int64_t span = (int64_t)(d.kv.num_pages - 1) * p.k_page_stride +
+                       (int64_t)(d.kv.page_tokens - 1) * p.k_token_stride +
+                       (int64_t)(d.kv.num_kv_heads - 1) * p.k_head_stride;
+  p.near_rows = p.k_page_stride == p.v_page_stride && p.k_token_stride == p.v_token_stride &&
+                p.k_head_stride == p.v_head_stride && span < (1LL << 36);
   const int grid = info.num_sms < kMaxGrid ? info.num_sms : kMaxGrid;
   const bool f16 = d.kv.dtype == QSA_HALF_F16;
   if (d.kv.head_dim == 128) return f16 ? launch_d<true, 128>(p, mt, info.device, grid, stream) : launch_d<false, 128>(p, mt, info.device, grid, stream);
