@@ -146,9 +146,12 @@ __global__ void __launch_bounds__(kNT, 1)
   const int c = (int)blockIdx.x;
   if (threadIdx.x == 0) p.meta[c * kMetaWords] = 0;
 
+  // Registers: 384 threads of 168 at launch, of which the first four warps
+  // leave some to the softmax warps (128 * 56 + 256 * 224 is the same sum).
   if (s.u0 < s.u1) {
-    Walker w(p, sched_sh, s.u0);
     if (warp == 0) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      Walker w(p, sched_sh, s.u0);
       // ------------------------------------------------------------ copies
       const int box = min(p.page_tokens, kUnit);
       uint32_t r = 0, items = 0;
@@ -207,6 +210,8 @@ __global__ void __launch_bounds__(kNT, 1)
         }
       }
     } else if (warp == 1) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      Walker w(p, sched_sh, s.u0);
       // ------------------------------------------------------------ products
       constexpr uint32_t id_qk = F16 ? ptx::idesc_f16_f32(128, 128) : ptx::idesc_bf16_f32(128, 128);
       constexpr uint32_t id_pv = (F16 ? ptx::idesc_f16_f32(128, D) : ptx::idesc_bf16_f32(128, D)) | ptx::kIdescBMnMajor;
@@ -287,7 +292,11 @@ __global__ void __launch_bounds__(kNT, 1)
         while (!ptx::mbar_try_wait(done, 0) && clock64() - t0 < kSpin) {
         }
       }
-    } else if (warp >= 4) {
+    } else if (warp < 4) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+      Walker w(p, sched_sh, s.u0);
       // ------------------------------------------------------------ softmax and epilogue
       const int st = (warp - 4) >> 2;
       const int row = ((warp & 3) << 5) + lane;
