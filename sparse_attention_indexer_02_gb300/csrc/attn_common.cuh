@@ -1,7 +1,7 @@
 // Parameters and the work schedule shared by the two forms of
 // qsa_paged_attention (attn_gather.cu, attn_tile.cu).
 //
-// Work is counted in units of `unit` keys (128, or 192) of one item; an item is a group of
+// Work is counted in units of 128 keys of one item; an item is a group of
 // query rows that share their keys: `tpi` consecutive new tokens of a request
 // times the query heads of a (virtual) key/value head.  The items of a call,
 // request by request, then head by head, then along the tokens, form one list
@@ -23,6 +23,7 @@
 namespace qsa {
 namespace attn {
 
+constexpr int kUnit = 128;      // keys a unit
 constexpr int kMaxGrid = 160;   // CTAs a launch, at most (GB300 has 152 SMs)
 static_assert(kMaxGrid * 4 == QSA_ATTN_COUNTER_BYTES, "one counter a CTA");
 constexpr float kLn2 = 0.6931471805599453f;
@@ -59,14 +60,44 @@ __device__ __forceinline__ int32_t keys_of(const AttnParams& p, const Request& r
   return min(max(r.pos0 + i1, 0), p.capacity);
 }
 
-__device__ __forceinline__ int32_t units_of(const AttnParams& p, int32_t keys) {
-  return max(1, (keys + p.unit - 1) / p.unit);
+__device__ __forceinline__ int32_t units_of(int32_t keys) { return max(1, (keys + kUnit - 1) / kUnit); }
+
+// a / b of non-negative values; in 32 bits when they allow it (a 64-bit
+// division is some hundred instructions).
+__device__ __forceinline__ int64_t div_nn(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
 }
 
-// Units of one head of a request: the sum over its items.
+__device__ __forceinline__ int32_t tiles_of(const AttnParams& p, int32_t n) { return (n + p.tpi - 1) / p.tpi; }
+
+// Units of tile t of a request: of the tokens [t * tpi, (t + 1) * tpi).
+__device__ __forceinline__ int32_t tile_units(const AttnParams& p, const Request& r, int32_t t) {
+  return units_of(keys_of(p, r, min((t + 1) * p.tpi, r.n)));
+}
+
+// Units of one head of each lane's request (n = 0: none), by the whole warp: a
+// lane adds up a few tiles itself, many are shared out over the lanes.
 __device__ __forceinline__ int64_t head_units(const AttnParams& p, const Request& r) {
+  constexpr int32_t kAlone = 4;
+  const int lane = (int)threadIdx.x & 31;
+  const int32_t tiles = tiles_of(p, r.n);
   int64_t u = 0;
-  for (int i = 0; i < r.n; i += p.tpi) u += units_of(p, keys_of(p, r, min(i + p.tpi, r.n)));
+  if (tiles <= kAlone)
+    for (int32_t t = 0; t < tiles; ++t) u += tile_units(p, r, t);
+  uint32_t many = __ballot_sync(0xffffffffu, tiles > kAlone);
+  while (many) {
+    const int src = __ffs(many) - 1;
+    many &= many - 1;
+    Request q;
+    q.n = __shfl_sync(0xffffffffu, r.n, src);
+    q.pos0 = __shfl_sync(0xffffffffu, r.pos0, src);
+    int64_t part = 0;
+    for (int32_t t = lane; t < tiles_of(p, q.n); t += 32) part += tile_units(p, q, t);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (lane == src) u = part;
+  }
   return u;
 }
 
@@ -79,105 +110,139 @@ struct Item {
   int64_t s0, s1;    // the item's units in the call's list
 };
 
-// The schedule of a launch; made by every thread of a CTA together.
+// How the list is shared out: the first `more` CTAs take each + 1 units, the others `each`.
 struct Schedule {
-  int64_t total;
-  int32_t ge;        // CTAs that take part
+  int64_t total, each;
+  int32_t ge, more;  // CTAs that take part
   int64_t u0, u1;    // this CTA's units
 
-  __device__ __forceinline__ int64_t share(int c) const { return total * c / ge; }
+  __device__ __forceinline__ void share_out(int64_t units, int32_t min_units) {
+    total = units;
+    ge = (int32_t)min((int64_t)gridDim.x, max((int64_t)1, div_nn(total, min_units)));
+    each = div_nn(total, ge);
+    more = (int32_t)(total - each * ge);
+    const int c = (int)blockIdx.x;
+    u0 = c < ge ? share(c) : total;
+    u1 = c < ge ? share(c + 1) : total;
+  }
+  __device__ __forceinline__ int64_t share(int c) const { return c * each + min(c, more); }
   // The CTA whose share holds unit u.
   __device__ __forceinline__ int owner(int64_t u) const {
-    int c = (int)min((int64_t)(ge - 1), u * ge / total);
-    while (c + 1 < ge && share(c + 1) <= u) ++c;
-    while (c > 0 && share(c) > u) --c;
-    return c;
+    const int64_t cut = more * (each + 1);
+    return u < cut ? (int)div_nn(u, each + 1) : more + (int)div_nn(u - cut, each);
   }
 };
 
 struct SchedShared {
   int64_t warp_sum[32];
-  int64_t base;   // units before the first request of this CTA's share
-  int32_t b;      // that request
+  int64_t base;      // units before the first request of this CTA's share
+  int64_t per_head;  // units of one head of that request
+  int32_t b;         // that request
 };
 
-// Builds the schedule over the requests' lengths: each thread sums a
-// contiguous run of requests, a block scan orders the runs, and the thread
-// whose run holds the CTA's first unit finds its request.
+// Builds the schedule over the requests' lengths, NT requests a round: a
+// thread a request, a block scan orders them, and the thread whose request
+// holds the CTA's first unit says so.  Up to NT requests the second pass works
+// on what the first has in registers.
 template <int NT>
 __device__ __forceinline__ Schedule make_schedule(const AttnParams& p, SchedShared& sh) {
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = p.num_requests;
-  const int per = (B + NT - 1) / NT;
-  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-  int64_t sum = 0;
-  for (int b = b0; b < b1; ++b) sum += head_units(p, request_of(p, b)) * p.hv;
-  int64_t incl = sum;
+  int64_t head = 0, before = 0, sum = 0;  // of this thread's request; of the rounds so far
+  auto round = [&](int b0) {
+    Request r = {0, 0, 0};
+    if (b0 + tid < B) r = request_of(p, b0 + tid);
+    head = head_units(p, r);
+    const int64_t mine = head * p.hv;
+    int64_t incl = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t a = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += a;
-  }
-  if (lane == 31) sh.warp_sum[warp] = incl;
-  if (tid == 0) sh.b = B, sh.base = 0;
-  __syncthreads();
-  int64_t before = incl - sum, total = 0;
-  for (int w = 0; w < NT / 32; ++w) {
-    if (w < warp) before += sh.warp_sum[w];
-    total += sh.warp_sum[w];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t a = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += a;
+    }
+    if (lane == 31) sh.warp_sum[warp] = incl;
+    __syncthreads();
+    before = sum + incl - mine;
+    for (int w = 0; w < NT / 32; ++w) {
+      const int64_t v = sh.warp_sum[w];
+      if (w < warp) before += v;
+      sum += v;
+    }
+  };
+  round(0);
+  for (int b0 = NT; b0 < B; b0 += NT) {
+    __syncthreads();
+    round(b0);
   }
   Schedule s;
-  s.total = total;
-  const int64_t want = (total + p.min_units - 1) / p.min_units;
-  s.ge = (int)min((int64_t)gridDim.x, max((int64_t)1, want));
-  const int c = (int)blockIdx.x;
-  s.u0 = c < s.ge ? s.share(c) : total;
-  s.u1 = c < s.ge ? s.share(c + 1) : total;
-  if (s.u0 < s.u1 && before <= s.u0 && s.u0 < before + sum) {
-    int64_t base = before;
-    for (int b = b0; b < b1; ++b) {
-      const int64_t u = head_units(p, request_of(p, b)) * p.hv;
-      if (s.u0 < base + u) {
-        sh.b = b;
-        sh.base = base;
-        break;
-      }
-      base += u;
+  s.share_out(sum, p.min_units);
+  auto look = [&](int b0) {
+    const int64_t mine = head * p.hv;
+    if (s.u0 < s.u1 && before <= s.u0 && s.u0 < before + mine) {
+      sh.b = b0 + tid;
+      sh.base = before;
+      sh.per_head = head;
+    }
+  };
+  if (B <= NT) {
+    look(0);
+  } else {
+    sum = 0;
+    for (int b0 = 0; b0 < B; b0 += NT) {
+      __syncthreads();
+      round(b0);
+      look(b0);
     }
   }
   __syncthreads();
   return s;
 }
 
-// Walks the items of the list from the one that holds unit u0.
+// Walks the items of the list from the one that holds unit u0; made and moved
+// by whole warps.
 struct Walker {
   const AttnParams& p;
   Item it;
   Request r;
 
+  __device__ __forceinline__ Walker(const AttnParams& p_, const Item& at) : p(p_), it(at), r(request_of(p_, at.b)) {}
   __device__ __forceinline__ Walker(const AttnParams& p_, const SchedShared& sh, int64_t u0) : p(p_) {
+    const int lane = (int)threadIdx.x & 31;
     it.b = sh.b;
     r = request_of(p, it.b);
-    const int64_t per_head = head_units(p, r);
     int64_t rem = u0 - sh.base;
-    it.hv = (int32_t)(rem / per_head);
-    rem -= it.hv * per_head;
-    int64_t s = u0 - rem;
-    it.i0 = 0;
-    for (;;) {
-      set();
-      const int32_t u = units_of(p, it.keys);
-      if (rem < u) {
-        it.s0 = s;
-        it.s1 = s + u;
-        return;
+    it.hv = (int32_t)div_nn(rem, sh.per_head);
+    rem -= it.hv * sh.per_head;
+    int64_t s = u0 - rem;  // the head's first unit
+    const int32_t tiles = tiles_of(p, r.n);
+    for (int32_t t0 = 0;; t0 += 32) {  // 32 tiles at a time: the one that holds the unit
+      const int32_t u = t0 + lane < tiles ? tile_units(p, r, t0 + lane) : 0;
+      int32_t incl = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t a = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += a;
       }
-      rem -= u;
-      s += u;
-      it.i0 += p.tpi;
+      const uint32_t past = __ballot_sync(0xffffffffu, rem < incl);
+      if (past) {
+        const int src = __ffs(past) - 1;
+        const int32_t n = __shfl_sync(0xffffffffu, u, src), z = __shfl_sync(0xffffffffu, incl, src);
+        it.i0 = (t0 + src) * p.tpi;
+        it.s1 = s + z;
+        it.s0 = it.s1 - n;
+        break;
+      }
+      const int32_t all = __shfl_sync(0xffffffffu, incl, 31);
+      rem -= all;
+      s += all;
+      if (t0 + 32 >= tiles) {  // not reached: the head holds the unit
+        it.i0 = 0;
+        it.s0 = it.s1 = s;
+        break;
+      }
     }
+    set();
   }
-  __device__ __forceinline__ Walker(const AttnParams& p_, const Item& at) : p(p_), it(at), r(request_of(p_, at.b)) {}
   __device__ __forceinline__ void set() {
     it.n = min(p.tpi, r.n - it.i0);
     it.row0 = r.first + it.i0;
@@ -197,7 +262,7 @@ struct Walker {
     }
     set();
     it.s0 = it.s1;
-    it.s1 += units_of(p, it.keys);
+    it.s1 += units_of(it.keys);
   }
 };
 

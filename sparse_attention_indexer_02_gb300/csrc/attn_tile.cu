@@ -51,7 +51,6 @@ namespace attn {
 namespace {
 
 constexpr int kNT = 384;
-constexpr int kUnit = 128;     // keys a tile, and a unit of the schedule
 constexpr int kRows = 128;     // query rows a stream
 constexpr int kMetaWords = 8;  // of a split item: parts, first row, tokens, virtual head
 constexpr float kRaise = 8.0f;
@@ -581,7 +580,6 @@ cudaError_t launch_attn_tile(AttnParams p, const qsa_attn_desc& d, uint8_t* work
   p.hv = d.kv.num_kv_heads;
   const int tpt = kRows / p.group;
   p.tpi = 2 * tpt;
-  p.unit = kUnit;
   p.min_units = 2;
   const CUtensorMapDataType ty = f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap qm, km, vm;
