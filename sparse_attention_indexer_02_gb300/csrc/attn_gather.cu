@@ -48,11 +48,19 @@ constexpr int kSlice = 16;       // keys a stage: one k-step of the second produ
 constexpr float kRaise = 8.0f;
 
 constexpr int kConsumers = kUnit / kSlice;  // warps; a slice of each unit each
-constexpr int kProducers = kConsumers / 2;  // warps; 32 rows of each unit each
 constexpr int kNC = 32 * kConsumers;
-constexpr int kNT = kNC + 32 * kProducers;
-constexpr int kStages = 3;
-static_assert(kConsumers == 8 && kProducers == 4, "register split and barrier counts");
+constexpr int kStages = 2;
+
+// Producer warps and the register split.  A warp issues one copy instruction
+// in about 70 cycles, so four producers move 28 bytes a cycle, below what L2
+// delivers: one row tile, whose consumers leave the registers, takes a producer
+// for each consumer.  With two tiles a producer serves two consumers.
+template <int MT>
+struct Conf {
+  static constexpr bool kOwn = MT == 1;  // a producer for each consumer
+  static constexpr int kProducers = kOwn ? kConsumers : kConsumers / 2;
+  static constexpr int kNT = kNC + 32 * kProducers;
+};
 
 template <int D, int MT>
 struct Layout {
@@ -64,7 +72,8 @@ struct Layout {
   static constexpr int kQ = kRows * kRow;
   static constexpr int q = kConsumers * kRing;             // two, by turns
   static constexpr int ml = q + 2 * kQ;                    // [warp][row] of (m, l)
-  static constexpr int bars = ml + kConsumers * kRows * 8; // full, empty [warp][stage], q full, q empty [2]
+  static constexpr int items = ml + kConsumers * kRows * 8;  // two ItemInfo, by turns
+  static constexpr int bars = items + 2 * 48;              // full, empty [warp][stage], q full, q empty [2]
   static constexpr int masks = bars + (2 * kConsumers * kStages + 4) * 8;  // [warp][stage]
   static constexpr int total = masks + kConsumers * kStages * 4;
   static_assert(16 * kMergeRow * 4 <= kStage, "16 rows of a warp's o fit a stage");
@@ -95,15 +104,26 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// 16 bytes to shared memory; zeros, nothing read, when `bytes` is 0.
+// 16 bytes to shared memory; zeros, nothing read, when `bytes` is 0.  Through
+// L1: past it (.cg) the same copies of random 256-byte rows moved half as much
+// again from L2 (5.98 GB for 3.98) and ran at 11.2 TB/s of rows against 15.7.
 __device__ __forceinline__ void copy16(uint32_t dst, uint64_t src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 // Arrives on `bar` when this thread's copies so far have landed (one of the barrier's expected arrivals).
 __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void copies_drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ bool consumers_any(bool mine) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)mine), "n"(kNC)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kNC) : "memory"); }
 
 // An unfinished part: o [kRows][D] floats, then (m, l) of each row.
@@ -136,23 +156,21 @@ __device__ __forceinline__ Item selected_item(const AttnParams& p, int64_t u, in
   return it;
 }
 
-// This CTA's part of an item, and the query heads of its virtual head.
-struct Part {
-  int ua, uz;   // units [ua, uz) of the item
-  int kvh, head0, gs;
-  __device__ __forceinline__ Part(const AttnParams& p, const Schedule& s, const Item& it) {
-    ua = (int)(max(s.u0, it.s0) - it.s0);
-    uz = (int)(min(s.u1, it.s1) - it.s0);
-    kvh = p.splits == 1 ? it.hv : it.hv / p.splits;
-    const int sub0 = (it.hv - kvh * p.splits) * p.sub;
-    gs = min(p.sub, p.group - sub0);
-    head0 = kvh * p.group + sub0;
-  }
+// What the consumers need of an item, from the producers.
+struct ItemInfo {
+  int32_t ua, uz;      // units [ua, uz) of the item are this CTA's
+  int32_t gs, head0;   // query heads of its virtual head
+  int32_t row0, n;     // rows of q
+  int32_t pos0, keys;
+  int32_t c0, c1;      // the CTAs it lies in
+  int32_t last;        // of this CTA
 };
 
 template <bool F16, int D, int MT, bool SEL>
-__global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const AttnParams p) {
   using L = Layout<D, MT>;
+  constexpr int kProducers = Conf<MT>::kProducers, kNT = Conf<MT>::kNT;
+  constexpr bool kOwn = Conf<MT>::kOwn;
   constexpr int kRows = L::kRows;
   constexpr int kChunks = D / 8;       // 16-byte chunks of a row
   constexpr int kRpi = 32 / kChunks;   // rows a copy instruction of the warp
@@ -167,13 +185,14 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
   uint64_t* q_empty = q_full + 2;
   volatile uint32_t* masks = reinterpret_cast<uint32_t*>(smem + L::masks);
   float2* ml = reinterpret_cast<float2*>(smem + L::ml);
+  static_assert(sizeof(ItemInfo) <= 48, "item slots");
   volatile int* abort_flag = &abort_sh;
 
   if (tid < kConsumers * kStages) {
     ptx::mbar_init(&full[tid], 33);  // the producer warp's copies, and its lane 0 for the mask
     ptx::mbar_init(&empty[tid], 1);
   } else if (tid >= 32 && tid < 34) {
-    ptx::mbar_init(&q_full[tid - 32], 32 * kProducers);
+    ptx::mbar_init(&q_full[tid - 32], 32 * kProducers + 1);
     ptx::mbar_init(&q_empty[tid - 32], kConsumers);
   }
   if (tid == 0) abort_sh = 0;
@@ -194,59 +213,73 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
     s = make_schedule<kNT>(p, sched_sh);
   }
   if (s.u0 >= s.u1) return;
-  auto first = [&]() -> Item {
-    if (SEL) return selected_item(p, s.u0, sel_units, 0);
-    return Walker(p, sched_sh, s.u0).it;
-  };
-  auto next = [&](Item& it) {
-    if (SEL) {
-      it = selected_item(p, it.s1, sel_units, it.b);
-    } else {
-      Walker w(p, it);
-      w.next();
-      it = w.it;
-    }
-  };
-
-  // Registers: 384 threads of 168 at launch; 128 * 88 + 256 * 208 is the same sum.
+  // Registers: 512 threads of 128 at launch, 256 * 72 + 256 * 176 are less; or
+  // 384 of 168, of which 128 * 88 + 256 * 208 is the same sum.
   if (warp >= kConsumers) {
     // ------------------------------------------------------------ producers
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (kOwn) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     const int pw = warp - kConsumers;
     const int chunk = lane % kChunks, sub_row = lane / kChunks;
-    uint32_t n = 0;  // slices filled, of either consumer
+    const int half = lane >> 4;
+    constexpr int kStep = kOwn ? 2 : 1;  // units an iteration
+    uint32_t n = 0;                      // slices filled, of any of its consumers
     bool ok = true;
-    Item it = first();
+    Item it;
+    if (SEL) it = selected_item(p, s.u0, sel_units, 0);
+    else it = Walker(p, sched_sh, s.u0).it;
     for (uint32_t k = 0; ok; ++k) {
-      const Part w(p, s, it);
+      const int ua = (int)(max(s.u0, it.s0) - it.s0), uz = (int)(min(s.u1, it.s1) - it.s0);
+      const int kvh = p.splits == 1 ? it.hv : it.hv / p.splits;
+      const int sub0 = (it.hv - kvh * p.splits) * p.sub;
+      const int gs = min(p.sub, p.group - sub0), head0 = kvh * p.group + sub0;
       // q: rows (token, head) into shared memory, the padding rows zero
       if (k >= 2) ok = __all_sync(0xffffffffu, wait_phase(&q_empty[k & 1], ((k >> 1) & 1u) ^ 1u, abort_flag, p.fault));
       if (!ok) break;
-      const int live = it.n * w.gs;
+      const int live = it.n * gs;
       for (int i = pw * 32 + lane; i < kRows * kChunks; i += 32 * kProducers) {
         const int r = i / kChunks, c = i - r * kChunks;
-        const int tk = r < live ? r / w.gs : 0, g = r < live ? r - tk * w.gs : 0;
+        const int tk = r < live ? r / gs : 0, g = r < live ? r - tk * gs : 0;
         copy16(ptx::smem_u32(smem + L::q) + (k & 1) * L::kQ + r * L::kRow + c * 16,
                reinterpret_cast<uint64_t>(p.q) + (uint64_t)((int64_t)(it.row0 + tk) * p.q_token_stride +
-                                                            (int64_t)(w.head0 + g) * p.q_head_stride + c * 16),
+                                                            (int64_t)(head0 + g) * p.q_head_stride + c * 16),
                r < live ? 16u : 0u);
       }
       copies_arrive(&q_full[k & 1]);
+      if (pw == 0 && lane == 0) {
+        ItemInfo* o = reinterpret_cast<ItemInfo*>(smem + L::items + (k & 1) * 48);
+        o->ua = ua;
+        o->uz = uz;
+        o->gs = gs;
+        o->head0 = head0;
+        o->row0 = it.row0;
+        o->n = it.n;
+        o->pos0 = it.pos0;
+        o->keys = it.keys;
+        o->c0 = it.s0 >= s.u0 ? (int)blockIdx.x : s.owner(it.s0);
+        o->c1 = it.s1 <= s.u1 ? (int)blockIdx.x : s.owner(it.s1 - 1);
+        o->last = it.s1 >= s.u1;
+        ptx::mbar_arrive(&q_full[k & 1]);
+      }
 
-      // the lane's place in unit j is j * 128 + pw * 32 + lane
+      // An iteration copies 32 rows: two units' slices of the warp's consumer, or a
+      // unit's slices of its two; a lane stands for place_of(j) in the list of keys.
+      auto place_of = [&](int j) -> int32_t {
+        return kOwn ? (j + half) * kUnit + pw * kSlice + (lane & 15) : j * kUnit + pw * 32 + lane;
+      };
+      auto in_share = [&](int j) -> bool { return (kOwn ? j + half : j) < uz; };
       const int32_t* table = p.block_table + (int64_t)it.b * p.table_stride;
       const int32_t* sel = SEL ? p.selected + (int64_t)it.row0 * p.num_selected : nullptr;
       const int32_t local0 = SEL ? it.pos0 + 1 - p.local_tokens : 0;  // first of the last tokens
       const int32_t keys = it.keys;
-      const int uz = w.uz;
       auto col_of = [&](int32_t at) -> int32_t { return p.ratio_shift >= 0 ? at >> p.ratio_shift : at / p.ratio; };
       auto entry_of = [&](int j) -> int32_t {  // SEL: the column listed for the place, -1 none
-        const int32_t at = j * kUnit + pw * 32 + lane;
-        return j < uz && at < sel_end ? __ldg(sel + col_of(at)) : -1;
+        const int32_t at = place_of(j);
+        return in_share(j) && at < sel_end ? __ldg(sel + col_of(at)) : -1;
       };
       auto token_of = [&](int j, int32_t col) -> int32_t {  // the token of the place, -1 none
-        const int32_t at = j * kUnit + pw * 32 + lane;
-        if (j >= uz) return -1;
+        const int32_t at = place_of(j);
+        if (!in_share(j)) return -1;
         if (!SEL) return at < keys ? at : -1;
         int64_t t;
         if (at < sel_end) {
@@ -261,22 +294,23 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
       auto page_of = [&](int32_t tok) -> int32_t {
         return tok < 0 ? 0 : __ldg(table + (p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_tokens));
       };
-      int32_t tok = token_of(w.ua, SEL ? entry_of(w.ua) : 0), page = page_of(tok);
-      int32_t col2 = SEL ? entry_of(w.ua + 1) : 0;
-      for (int j = w.ua; j < uz && ok; ++j, ++n) {
+      int32_t tok = token_of(ua, SEL ? entry_of(ua) : 0), page = page_of(tok);
+      int32_t col2 = SEL ? entry_of(ua + kStep) : 0;
+      for (int j = ua; j < uz && ok; j += kStep) {
         const uint32_t vm = __ballot_sync(0xffffffffu, tok >= 0);
         const int32_t pg = min(max(page, 0), p.num_pages - 1), tk = max(tok, 0);
         const int32_t off = p.page_shift >= 0 ? tk & (p.page_tokens - 1) : tk % p.page_tokens;
-        const int64_t ko = (int64_t)w.kvh * p.k_head_stride + (int64_t)pg * p.k_page_stride + (int64_t)off * p.k_token_stride;
-        const int64_t vo = p.near_rows ? 0 : (int64_t)w.kvh * p.v_head_stride + (int64_t)pg * p.v_page_stride +
+        const int64_t ko = (int64_t)kvh * p.k_head_stride + (int64_t)pg * p.k_page_stride + (int64_t)off * p.k_token_stride;
+        const int64_t vo = p.near_rows ? 0 : (int64_t)kvh * p.v_head_stride + (int64_t)pg * p.v_page_stride +
                                                  (int64_t)off * p.v_token_stride;
-        tok = token_of(j + 1, col2);
+        tok = token_of(j + kStep, col2);
         page = page_of(tok);
-        if (SEL) col2 = entry_of(j + 2);
-        const uint32_t st = n % kStages;
+        if (SEL) col2 = entry_of(j + 2 * kStep);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int cw = 2 * pw + h;
+          if (kOwn && j + h >= uz) break;
+          const int cw = kOwn ? pw : 2 * pw + h;
+          const uint32_t st = n % kStages;
           if (n >= kStages)
             ok = __all_sync(0xffffffffu, wait_phase(&empty[cw * kStages + st], ((n / kStages) & 1u) ^ 1u, abort_flag,
                                                     p.fault));
@@ -308,26 +342,34 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
             masks[cw * kStages + st] = (vm >> (h * kSlice)) & 0xFFFFu;
             ptx::mbar_arrive(&full[cw * kStages + st]);
           }
+          if (kOwn || h == 1) ++n;
         }
       }
       if (!ok || it.s1 >= s.u1) break;
-      next(it);
+      if (SEL) {
+        it = selected_item(p, it.s1, sel_units, it.b);
+      } else {
+        Walker w(p, it);
+        w.next();
+        it = w.it;
+      }
     }
     copies_drain();
   } else {
     // ------------------------------------------------------------ consumers
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if (kOwn) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     uint64_t* my_full = full + warp * kStages;
     uint64_t* my_empty = empty + warp * kStages;
     uint8_t* ring = smem + warp * L::kRing;
     uint32_t used = 0;
     bool ok = true;
-    Item it = first();
     for (uint32_t k = 0;; ++k) {
-      const Part w(p, s, it);
-      const int gs = w.gs, head0 = w.head0, live = it.n * w.gs;
-      const int64_t row0 = it.row0;
       if (ok) ok = __all_sync(0xffffffffu, wait_phase(&q_full[k & 1], (k >> 1) & 1u, abort_flag, p.fault));
+      if (consumers_any(!ok)) break;  // together: the item will not come
+      const ItemInfo it = *reinterpret_cast<const ItemInfo*>(smem + L::items + (k & 1) * 48);
+      const int gs = it.gs, head0 = it.head0, live = it.n * it.gs;
+      const int64_t row0 = it.row0;
       const uint32_t q_addr = ptx::smem_u32(smem + L::q) + (k & 1) * L::kQ + (lane & 15) * L::kRow +
                               (lane >> 4) * 16;  // row, 8-element half
       uint32_t qf[MT == 1 ? D / 16 : 1][4];
@@ -354,7 +396,7 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
         l[mt][0] = l[mt][1] = 0.0f;
       }
 
-      for (int j = w.ua; j < w.uz; ++j, ++used) {
+      for (int j = it.ua; j < it.uz; ++j, ++used) {
         const uint32_t st = used % kStages;
         if (ok) ok = __all_sync(0xffffffffu, wait_phase(&my_full[st], (used / kStages) & 1u, abort_flag, p.fault));
         const uint32_t vm = masks[warp * kStages + st];
@@ -402,19 +444,35 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
                   if (!seen) x[mt][n][e] = -INFINITY;
                 }
           }
-          uint32_t pa[MT][4];
+          // values: transposed loads, lanes 0-15 rows 0-15 of columns 0-7, lanes 16-31 of columns
+          // 8-15; one row tile has the registers to start them before the softmax
+          const uint32_t v_addr = kb + kSlice * L::kRow + (lane & 15) * L::kRow + (lane >> 4) * 16;
+          uint32_t bv[D / 16][4];
+          if (MT == 1) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
+            for (int i = 0; i < D / 16; ++i) ldsm4t(bv[i], v_addr + i * 32);
+          }
+          // m is raised when a maximum passes it by more than 8 only: any m that keeps the
+          // exponentials in range gives the same quotient, and raising costs a pass over o.
+          // So a row's lanes look at their own scores, and find the row's maximum only then.
+          float mx[MT][2];
+          bool raise = false;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              float mx = fmaxf(fmaxf(x[mt][0][2 * h], x[mt][0][2 * h + 1]), fmaxf(x[mt][1][2 * h], x[mt][1][2 * h + 1]));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-              mx *= p.scale_log2;
-              // m is raised when a maximum passes it by more than 8 only: any m that keeps
-              // the exponentials in range gives the same quotient, and raising costs a pass over o
-              if (__any_sync(0xffffffffu, mx > m[mt][h] + kRaise || (m[mt][h] == -INFINITY && mx > m[mt][h]))) {
-                const float mn = fmaxf(m[mt][h], mx);
+              mx[mt][h] = p.scale_log2 * fmaxf(fmaxf(x[mt][0][2 * h], x[mt][0][2 * h + 1]),
+                                               fmaxf(x[mt][1][2 * h], x[mt][1][2 * h + 1]));
+              raise = raise || mx[mt][h] > m[mt][h] + kRaise || (m[mt][h] == -INFINITY && mx[mt][h] > -INFINITY);
+            }
+          if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float t = fmaxf(mx[mt][h], __shfl_xor_sync(0xffffffffu, mx[mt][h], 1));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                const float mn = fmaxf(m[mt][h], t);
                 const float f = mn == -INFINITY ? 1.0f : ex2(m[mt][h] - mn);
                 m[mt][h] = mn;
                 l[mt][h] *= f;
@@ -424,6 +482,12 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
                   o[mt][i][2 * h + 1] *= f;
                 }
               }
+          }
+          uint32_t pa[MT][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
               const float sub = m[mt][h] == -INFINITY ? 0.0f : -m[mt][h];
               float pr[4];
 #pragma unroll
@@ -432,33 +496,37 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
               pa[mt][h] = pack2<F16>(pr[0], pr[1]);
               pa[mt][2 + h] = pack2<F16>(pr[2], pr[3]);
             }
-          }
-          // values: transposed loads, lanes 0-15 rows 0-15 of columns 0-7, lanes 16-31 of columns 8-15
-          const uint32_t v_addr = kb + kSlice * L::kRow + (lane & 15) * L::kRow + (lane >> 4) * 16;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            uint32_t bv[4];
-            ldsm4t(bv, v_addr + i * 32);
+            if (MT > 1) ldsm4t(bv[i], v_addr + i * 32);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-              mma16816<F16>(o[mt][2 * i], pa[mt], bv[0], bv[1]);
-              mma16816<F16>(o[mt][2 * i + 1], pa[mt], bv[2], bv[3]);
+              mma16816<F16>(o[mt][2 * i], pa[mt], bv[i][0], bv[i][1]);
+              mma16816<F16>(o[mt][2 * i + 1], pa[mt], bv[i][2], bv[i][3]);
             }
           }
         }
         __syncwarp();
         // the last slice's stage stays: the warps join in it
-        if (j + 1 < w.uz && lane == 0) ptx::mbar_arrive(&my_empty[st]);
+        if (j + 1 < it.uz && lane == 0) ptx::mbar_arrive(&my_empty[st]);
       }
       if (lane == 0) ptx::mbar_arrive(&q_empty[k & 1]);
 
-      // ---- join the warps, 16 rows at a time
+      // ---- join the warps: their maxima first, then o, each warp's on the common one, 16 rows at a time
       const uint32_t held = (used + kStages - 1) % kStages;
-      const int c = (int)blockIdx.x;
-      const int c0 = it.s0 >= s.u0 ? c : s.owner(it.s0);
-      const int c1 = it.s1 <= s.u1 ? c : s.owner(it.s1 - 1);
+      const int c = (int)blockIdx.x, c0 = it.c0, c1 = it.c1;
       const bool split = c0 != c1;
       float* part = p.parts + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * part_floats<D, MT>();
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float t = l[mt][h];
+          t += __shfl_xor_sync(0xffffffffu, t, 1);
+          t += __shfl_xor_sync(0xffffffffu, t, 2);
+          if ((lane & 3) == 0) ml[warp * kRows + mt * 16 + h * 8 + (lane >> 2)] = make_float2(m[mt][h], t);
+        }
+      consumers_sync();
       auto write_out = [&](int r, int d, float M, float Lsum, const float (&acc)[4]) {
         const int tk = r / gs, g = r - tk * gs;
         const int64_t row = row0 + tk;
@@ -472,35 +540,35 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
         if (mt > 0) consumers_sync();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float t = l[mt][h];
-          t += __shfl_xor_sync(0xffffffffu, t, 1);
-          t += __shfl_xor_sync(0xffffffffu, t, 2);
           const int r = h * 8 + (lane >> 2);
-          if ((lane & 3) == 0) ml[warp * kRows + mt * 16 + r] = make_float2(m[mt][h], t);
+          float M = m[mt][h];
+#pragma unroll
+          for (int x = 0; x < kConsumers; ++x) M = fmaxf(M, ml[x * kRows + mt * 16 + r].x);
+          const float f = M == -INFINITY ? 0.0f : ex2(m[mt][h] - M);
           float* dst = reinterpret_cast<float*>(ring + held * L::kStage) + r * L::kMergeRow + (lane & 3) * 2;
 #pragma unroll
           for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float2*>(dst + i * 8) = make_float2(o[mt][i][2 * h], o[mt][i][2 * h + 1]);
+            *reinterpret_cast<float2*>(dst + i * 8) = make_float2(o[mt][i][2 * h] * f, o[mt][i][2 * h + 1] * f);
         }
         consumers_sync();
         for (int i = tid; i < 16 * (D / 4); i += kNC) {
           const int rr = i / (D / 4), d = (i - rr * (D / 4)) * 4, r = mt * 16 + rr;
           if (r >= live) continue;
-          float M = -INFINITY;
+          float M = -INFINITY, Ls = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          float2 e[kConsumers];
 #pragma unroll
-          for (int x = 0; x < kConsumers; ++x) M = fmaxf(M, ml[x * kRows + r].x);
-          float Ls = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          for (int x = 0; x < kConsumers; ++x) e[x] = ml[x * kRows + r];
+#pragma unroll
+          for (int x = 0; x < kConsumers; ++x) M = fmaxf(M, e[x].x);
 #pragma unroll
           for (int x = 0; x < kConsumers; ++x) {
-            const float2 e = ml[x * kRows + r];
-            const float f = e.x == -INFINITY ? 0.0f : ex2(e.x - M);
             const float4 v = *reinterpret_cast<const float4*>(
                 reinterpret_cast<const float*>(smem + x * L::kRing + held * L::kStage) + rr * L::kMergeRow + d);
-            Ls += e.y * f;
-            acc[0] = fmaf(v.x, f, acc[0]);
-            acc[1] = fmaf(v.y, f, acc[1]);
-            acc[2] = fmaf(v.z, f, acc[2]);
-            acc[3] = fmaf(v.w, f, acc[3]);
+            Ls += e[x].x == -INFINITY ? 0.0f : e[x].y * ex2(e[x].x - M);
+            acc[0] += v.x;
+            acc[1] += v.y;
+            acc[2] += v.z;
+            acc[3] += v.w;
           }
           if (!split) {
             write_out(r, d, M, Ls, acc);
@@ -548,8 +616,7 @@ __global__ void __launch_bounds__(kNT, 1) attn_gather_kernel(const AttnParams p)
           }
         }
       }
-      if (it.s1 >= s.u1) break;
-      next(it);
+      if (it.last) break;
     }
   }
 }
@@ -563,7 +630,7 @@ cudaError_t launch_t(const AttnParams& p, int device, int grid, cudaStream_t str
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
-  cfg.blockDim = dim3(kNT, 1, 1);
+  cfg.blockDim = dim3(Conf<MT>::kNT, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
