@@ -68,7 +68,7 @@ struct Layout {
   static constexpr int kRow = 2 * D + 16;                  // bytes from row to row
   static constexpr int kStage = 2 * kSlice * kRow;         // key rows, then value rows
   static constexpr int kRing = kStages * kStage;           // of a consumer
-  static constexpr int kMergeRow = D + 4;                  // floats from row to row of a warp's o
+  static constexpr int kMergeRow = D + 8;                  // floats from row to row of a warp's o (8 rows: all banks)
   static constexpr int kQ = kRows * kRow;
   static constexpr int q = kConsumers * kRing;             // two, by turns
   static constexpr int ml = q + 2 * kQ;                    // [warp][row] of (m, l)
@@ -233,35 +233,6 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
       const int kvh = p.splits == 1 ? it.hv : it.hv / p.splits;
       const int sub0 = (it.hv - kvh * p.splits) * p.sub;
       const int gs = min(p.sub, p.group - sub0), head0 = kvh * p.group + sub0;
-      // q: rows (token, head) into shared memory, the padding rows zero
-      if (k >= 2) ok = __all_sync(0xffffffffu, wait_phase(&q_empty[k & 1], ((k >> 1) & 1u) ^ 1u, abort_flag, p.fault));
-      if (!ok) break;
-      const int live = it.n * gs;
-      for (int i = pw * 32 + lane; i < kRows * kChunks; i += 32 * kProducers) {
-        const int r = i / kChunks, c = i - r * kChunks;
-        const int tk = r < live ? r / gs : 0, g = r < live ? r - tk * gs : 0;
-        copy16(ptx::smem_u32(smem + L::q) + (k & 1) * L::kQ + r * L::kRow + c * 16,
-               reinterpret_cast<uint64_t>(p.q) + (uint64_t)((int64_t)(it.row0 + tk) * p.q_token_stride +
-                                                            (int64_t)(head0 + g) * p.q_head_stride + c * 16),
-               r < live ? 16u : 0u);
-      }
-      copies_arrive(&q_full[k & 1]);
-      if (pw == 0 && lane == 0) {
-        ItemInfo* o = reinterpret_cast<ItemInfo*>(smem + L::items + (k & 1) * 48);
-        o->ua = ua;
-        o->uz = uz;
-        o->gs = gs;
-        o->head0 = head0;
-        o->row0 = it.row0;
-        o->n = it.n;
-        o->pos0 = it.pos0;
-        o->keys = it.keys;
-        o->c0 = it.s0 >= s.u0 ? (int)blockIdx.x : s.owner(it.s0);
-        o->c1 = it.s1 <= s.u1 ? (int)blockIdx.x : s.owner(it.s1 - 1);
-        o->last = it.s1 >= s.u1;
-        ptx::mbar_arrive(&q_full[k & 1]);
-      }
-
       // An iteration copies 32 rows: two units' slices of the warp's consumer, or a
       // unit's slices of its two; a lane stands for place_of(j) in the list of keys.
       auto place_of = [&](int j) -> int32_t {
@@ -296,6 +267,35 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
       };
       int32_t tok = token_of(ua, SEL ? entry_of(ua) : 0), page = page_of(tok);
       int32_t col2 = SEL ? entry_of(ua + kStep) : 0;
+      // q: rows (token, head) into shared memory, the padding rows zero
+      if (k >= 2) ok = __all_sync(0xffffffffu, wait_phase(&q_empty[k & 1], ((k >> 1) & 1u) ^ 1u, abort_flag, p.fault));
+      if (!ok) break;
+      const int live = it.n * gs;
+      for (int i = pw * 32 + lane; i < kRows * kChunks; i += 32 * kProducers) {
+        const int r = i / kChunks, c = i - r * kChunks;
+        const int tk = r < live ? r / gs : 0, g = r < live ? r - tk * gs : 0;
+        copy16(ptx::smem_u32(smem + L::q) + (k & 1) * L::kQ + r * L::kRow + c * 16,
+               reinterpret_cast<uint64_t>(p.q) + (uint64_t)((int64_t)(it.row0 + tk) * p.q_token_stride +
+                                                            (int64_t)(head0 + g) * p.q_head_stride + c * 16),
+               r < live ? 16u : 0u);
+      }
+      copies_arrive(&q_full[k & 1]);
+      if (pw == 0 && lane == 0) {
+        ItemInfo* o = reinterpret_cast<ItemInfo*>(smem + L::items + (k & 1) * 48);
+        o->ua = ua;
+        o->uz = uz;
+        o->gs = gs;
+        o->head0 = head0;
+        o->row0 = it.row0;
+        o->n = it.n;
+        o->pos0 = it.pos0;
+        o->keys = it.keys;
+        o->c0 = it.s0 >= s.u0 ? (int)blockIdx.x : s.owner(it.s0);
+        o->c1 = it.s1 <= s.u1 ? (int)blockIdx.x : s.owner(it.s1 - 1);
+        o->last = it.s1 >= s.u1;
+        ptx::mbar_arrive(&q_full[k & 1]);
+      }
+
       for (int j = ua; j < uz && ok; j += kStep) {
         const uint32_t vm = __ballot_sync(0xffffffffu, tok >= 0);
         const int32_t pg = min(max(page, 0), p.num_pages - 1), tk = max(tok, 0);
