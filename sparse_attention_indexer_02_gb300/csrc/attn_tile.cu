@@ -93,6 +93,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 template <bool F16, int D>
 __global__ void __launch_bounds__(kNT, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
@@ -146,10 +152,10 @@ __global__ void __launch_bounds__(kNT, 1)
   if (threadIdx.x == 0) p.meta[c * kMetaWords] = 0;
 
   // Registers: 384 threads of 168 at launch, of which the first four warps
-  // leave some to the softmax warps (128 * 56 + 256 * 224 is the same sum).
+  // leave some to the softmax warps (128 * 72 + 256 * 216 is the same sum).
   if (s.u0 < s.u1) {
     if (warp == 0) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       Walker w(p, sched_sh, s.u0);
       // ------------------------------------------------------------ copies
       const int box = min(p.page_tokens, kUnit);
@@ -209,7 +215,7 @@ __global__ void __launch_bounds__(kNT, 1)
         }
       }
     } else if (warp == 1) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       Walker w(p, sched_sh, s.u0);
       // ------------------------------------------------------------ products
       constexpr uint32_t id_qk = F16 ? ptx::idesc_f16_f32(128, 128) : ptx::idesc_bf16_f32(128, 128);
@@ -292,9 +298,9 @@ __global__ void __launch_bounds__(kNT, 1)
         }
       }
     } else if (warp < 4) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     } else {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
       Walker w(p, sched_sh, s.u0);
       // ------------------------------------------------------------ softmax and epilogue
       const int st = (warp - 4) >> 2;
@@ -319,28 +325,68 @@ __global__ void __launch_bounds__(kNT, 1)
             if (!ok) break;
             ptx::tc_fence_after();
             uint32_t x[4][32];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) ptx::tmem_ld32(t_s + q * 32, x[q]);
+            ptx::tmem_ld32(t_s, x[0]);
+            ptx::tmem_ld32(t_s + 32, x[1]);
             ptx::tmem_ld_wait();
+            ptx::tmem_ld_done32(x[0]);
+            ptx::tmem_ld_done32(x[1]);
+            ptx::tmem_ld32(t_s + 64, x[2]);  // on their way while the first half is worked on
+            ptx::tmem_ld32(t_s + 96, x[3]);
             const int seen = lim - j * kUnit;
-            if (__any_sync(0xffffffffu, seen < kUnit)) {
+            const bool edge = __any_sync(0xffffffffu, seen < kUnit);
+            float top[4];
+            uint64_t sum[2];
+            auto mask = [&](int q) {
+              if (!edge) return;
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
+              for (int i = 0; i < 32; ++i)
+                if (q * 32 + i >= seen) x[q][i] = 0xFF800000u;
+            };
+            auto max_of = [&](int q) {
+              float t[2] = {__uint_as_float(x[q][0]), __uint_as_float(x[q][1])};
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (q * 32 + i >= seen) x[q][i] = 0xFF800000u;
-            }
-            float mx[4];
+              for (int i = 2; i < 30; i += 4) {
+                t[0] = max3(t[0], __uint_as_float(x[q][i]), __uint_as_float(x[q][i + 1]));
+                t[1] = max3(t[1], __uint_as_float(x[q][i + 2]), __uint_as_float(x[q][i + 3]));
+              }
+              top[q] = fmaxf(max3(t[0], __uint_as_float(x[q][30]), __uint_as_float(x[q][31])), t[1]);
+            };
+            // columns 64 h .. 64 h + 63: 2^(x * sc - m * sc), their sum, and as 16-bit pairs into TMEM
+            auto probabilities = [&](int h, float neg) {
+              const uint64_t neg2 = pack_f32x2(neg, neg);
+              uint32_t pk[32];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              mx[q] = __uint_as_float(x[q][0]);
-#pragma unroll
-              for (int i = 1; i < 32; ++i) mx[q] = fmaxf(mx[q], __uint_as_float(x[q][i]));
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            // raise m (for m = -inf: to any maximum)
-            if (__any_sync(0xffffffffu, top > m + raise || (m == -INFINITY && top > m))) {
-              const float mn = fmaxf(m, top);
+              for (int i = 0; i < 32; ++i) {
+                const uint32_t* xs = &x[2 * h + (i >> 4)][(2 * i) & 31];
+                float a, b;
+                unpack_f32x2(fma2(pack_f32x2(__uint_as_float(xs[0]), __uint_as_float(xs[1])), sc2, neg2), a, b);
+                a = ex2(a);
+                b = ex2(b);
+                sum[i & 1] = add2(sum[i & 1], pack_f32x2(a, b));
+                pk[i] = pack2<F16>(a, b);
+              }
+              ptx::tmem_st32(t_s + h * 32, pk);
+            };
+            // With the m there is, while the maxima are taken along: that m stands unless a
+            // row's maximum passes it by more than 8, seldom after an item's first tiles.
+            float neg = m == -INFINITY ? 0.0f : -m * sc;
+            sum[0] = sum[1] = 0;
+            mask(0);
+            mask(1);
+            if (j > ua) probabilities(0, neg);
+            max_of(0);
+            max_of(1);
+            ptx::tmem_ld_wait();
+            ptx::tmem_ld_done32(x[2]);
+            ptx::tmem_ld_done32(x[3]);
+            mask(2);
+            mask(3);
+            if (j > ua) probabilities(1, neg);
+            max_of(2);
+            max_of(3);
+            const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            if (__any_sync(0xffffffffu, j == ua || tile_top > m + raise || (m == -INFINITY && tile_top > m))) {
+              const float mn = fmaxf(m, tile_top);
               const float f = mn == -INFINITY ? 1.0f : ex2((m - mn) * sc);
               m = mn;
               l *= f;
@@ -350,29 +396,16 @@ __global__ void __launch_bounds__(kNT, 1)
                   uint32_t o[32];
                   ptx::tmem_ld32(t_o + q * 32, o);
                   ptx::tmem_ld_wait();
+                  ptx::tmem_ld_done32(o);
 #pragma unroll
                   for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                   ptx::tmem_st32(t_o + q * 32, o);
                 }
               }
-            }
-            const float neg = m == -INFINITY ? 0.0f : -m * sc;
-            const uint64_t neg2 = pack_f32x2(neg, neg);
-            uint64_t sum[2] = {0, 0};
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t pk[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const uint32_t* xs = &x[2 * q + (i >> 4)][(2 * i) & 31];
-                float a, b;
-                unpack_f32x2(fma2(pack_f32x2(__uint_as_float(xs[0]), __uint_as_float(xs[1])), sc2, neg2), a, b);
-                a = ex2(a);
-                b = ex2(b);
-                sum[i & 1] = add2(sum[i & 1], pack_f32x2(a, b));
-                pk[i] = pack2<F16>(a, b);
-              }
-              ptx::tmem_st32(t_s + q * 32, pk);
+              neg = m == -INFINITY ? 0.0f : -m * sc;
+              sum[0] = sum[1] = 0;
+              probabilities(0, neg);
+              probabilities(1, neg);
             }
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
