@@ -5,12 +5,14 @@
 // query rows that share their keys: `tpi` consecutive new tokens of a request
 // times the query heads of a (virtual) key/value head.  The items of a call,
 // request by request, then head by head, then along the tokens, form one list
-// of units, and CTA c of `ge` takes the units [total * c / ge, total * (c+1) /
-// ge): every CTA has the same work to within a unit whatever the lengths are,
-// one long request among short ones included, and an item whose units lie in
-// several CTAs is joined from their parts (partial sums with their running
-// maximum and sum).  A CTA has at most two unfinished parts, the one it begins
-// with and the one it ends with, so the workspace is two parts a CTA.
+// of units, of which each of the launch's CTAs takes an equal, contiguous
+// share: every CTA has the same work to within a unit whatever the lengths are,
+// one long request among short ones included.  An item counts item_cost units
+// behind those of its keys, for its start and its end: without them the CTAs
+// that get many short items finish last.  An item whose units lie in several
+// CTAs is joined from their parts (partial sums with their running maximum and
+// sum).  A CTA has at most two unfinished parts, the one it begins with and the
+// one it ends with, so the workspace is two parts a CTA.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -61,6 +63,7 @@ __device__ __forceinline__ int32_t keys_of(const AttnParams& p, const Request& r
 }
 
 __device__ __forceinline__ int32_t units_of(int32_t keys) { return max(1, (keys + kUnit - 1) / kUnit); }
+__device__ __forceinline__ int32_t item_units(const AttnParams& p, int32_t keys) { return units_of(keys) + p.item_cost; }
 
 // a / b of non-negative values; in 32 bits when they allow it (a 64-bit
 // division is some hundred instructions).
@@ -73,7 +76,7 @@ __device__ __forceinline__ int32_t tiles_of(const AttnParams& p, int32_t n) { re
 
 // Units of tile t of a request: of the tokens [t * tpi, (t + 1) * tpi).
 __device__ __forceinline__ int32_t tile_units(const AttnParams& p, const Request& r, int32_t t) {
-  return units_of(keys_of(p, r, min((t + 1) * p.tpi, r.n)));
+  return item_units(p, keys_of(p, r, min((t + 1) * p.tpi, r.n)));
 }
 
 // Units of one head of each lane's request (n = 0: none), by the whole warp: a
@@ -116,9 +119,9 @@ struct Schedule {
   int32_t ge, more;  // CTAs that take part
   int64_t u0, u1;    // this CTA's units
 
-  __device__ __forceinline__ void share_out(int64_t units, int32_t min_units) {
+  __device__ __forceinline__ void share_out(int64_t units, int32_t min_shift) {
     total = units;
-    ge = (int32_t)min((int64_t)gridDim.x, max((int64_t)1, div_nn(total, min_units)));
+    ge = (int32_t)min((int64_t)gridDim.x, max((int64_t)1, total >> min_shift));
     each = div_nn(total, ge);
     more = (int32_t)(total - each * ge);
     const int c = (int)blockIdx.x;
@@ -133,33 +136,90 @@ struct Schedule {
   }
 };
 
-struct SchedShared {
-  int64_t warp_sum[32];
-  int64_t base;      // units before the first request of this CTA's share
-  int64_t per_head;  // units of one head of that request
-  int32_t b;         // that request
+// A CTA's part of an item: its units [a, z) of the item's keys.  An item's keys
+// come before its item_cost, so only the first item of a share can be one the
+// CTA has no part in (a >= z).
+struct Part {
+  int32_t a, z;
+  __device__ __forceinline__ Part(const AttnParams& p, const Schedule& s, const Item& it) {
+    a = (int32_t)(max(s.u0, it.s0) - it.s0);
+    z = (int32_t)(min(s.u1, it.s1 - p.item_cost) - it.s0);
+  }
+};
+// The first and the last CTA that have a part of the item, given that this one has.
+__device__ __forceinline__ int first_cta(const Schedule& s, const Item& it) {
+  return it.s0 >= s.u0 ? (int)blockIdx.x : s.owner(it.s0);
+}
+__device__ __forceinline__ int last_cta(const AttnParams& p, const Schedule& s, const Item& it) {
+  const int64_t end = it.s1 - p.item_cost;
+  return end <= s.u1 ? (int)blockIdx.x : s.owner(end - 1);
+}
+
+// What the warps that work on an item need of it, from the one that walks the list.
+struct ItemInfo {
+  int32_t a, z;        // the CTA's units of it
+  int32_t row0, n;     // rows of q
+  int32_t pos0, keys;
+  int32_t gs, head0;   // query heads of its virtual head
+  int32_t c0, c1;      // the CTAs that have a part of it
+  int32_t last;        // of this CTA
 };
 
-// Builds the schedule over the requests' lengths, NT requests a round: a
-// thread a request, a block scan orders them, and the thread whose request
-// holds the CTA's first unit says so.  Up to NT requests the second pass works
-// on what the first has in registers.
+struct SchedShared {
+  int64_t warp_sum[32];
+  int64_t base;      // as in Start
+  int64_t per_head;
+  int32_t b;
+};
+
+// Where a CTA's share begins: the request its first unit belongs to.
+struct Start {
+  int64_t base;      // units before that request
+  int64_t per_head;  // units of one head of it
+  int32_t b;
+  Request r;
+};
+
+// Builds the schedule over the requests' lengths; called by all NT threads, it
+// contains a CTA barrier.  Up to 32 requests every warp does it by itself, a
+// lane a request.  More: NT requests a round, a thread a request, ordered by a
+// block scan, and the thread whose request holds the CTA's first unit says so.
+// Up to NT requests the second pass works on what the first has in registers.
 template <int NT>
-__device__ __forceinline__ Schedule make_schedule(const AttnParams& p, SchedShared& sh) {
+__device__ __forceinline__ Schedule make_schedule(const AttnParams& p, SchedShared& sh, Start& at) {
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = p.num_requests;
+  Schedule s;
+  auto scan = [&](int64_t v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t a = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += a;
+    }
+    return v;
+  };
+  if (B <= 32) {
+    Request r = {0, 0, 0};
+    if (lane < B) r = request_of(p, lane);
+    const int64_t head = head_units(p, r), mine = head * p.hv, incl = scan(mine);
+    s.share_out(__shfl_sync(0xffffffffu, incl, 31), p.min_shift);
+    const uint32_t here = __ballot_sync(0xffffffffu, incl - mine <= s.u0 && s.u0 < incl);
+    const int src = here ? __ffs(here) - 1 : 0;
+    at.b = src;
+    at.base = __shfl_sync(0xffffffffu, incl - mine, src);
+    at.per_head = __shfl_sync(0xffffffffu, head, src);
+    at.r.first = __shfl_sync(0xffffffffu, r.first, src);
+    at.r.n = __shfl_sync(0xffffffffu, r.n, src);
+    at.r.pos0 = __shfl_sync(0xffffffffu, r.pos0, src);
+    __syncthreads();
+    return s;
+  }
   int64_t head = 0, before = 0, sum = 0;  // of this thread's request; of the rounds so far
   auto round = [&](int b0) {
     Request r = {0, 0, 0};
     if (b0 + tid < B) r = request_of(p, b0 + tid);
     head = head_units(p, r);
-    const int64_t mine = head * p.hv;
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t a = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += a;
-    }
+    const int64_t mine = head * p.hv, incl = scan(mine);
     if (lane == 31) sh.warp_sum[warp] = incl;
     __syncthreads();
     before = sum + incl - mine;
@@ -174,8 +234,7 @@ __device__ __forceinline__ Schedule make_schedule(const AttnParams& p, SchedShar
     __syncthreads();
     round(b0);
   }
-  Schedule s;
-  s.share_out(sum, p.min_units);
+  s.share_out(sum, p.min_shift);
   auto look = [&](int b0) {
     const int64_t mine = head * p.hv;
     if (s.u0 < s.u1 && before <= s.u0 && s.u0 < before + mine) {
@@ -195,6 +254,7 @@ __device__ __forceinline__ Schedule make_schedule(const AttnParams& p, SchedShar
     }
   }
   __syncthreads();
+  if (s.u0 < s.u1) at = {sh.base, sh.per_head, sh.b, request_of(p, sh.b)};
   return s;
 }
 
@@ -206,13 +266,13 @@ struct Walker {
   Request r;
 
   __device__ __forceinline__ Walker(const AttnParams& p_, const Item& at) : p(p_), it(at), r(request_of(p_, at.b)) {}
-  __device__ __forceinline__ Walker(const AttnParams& p_, const SchedShared& sh, int64_t u0) : p(p_) {
+  __device__ __forceinline__ Walker(const AttnParams& p_, const Item& at, const Request& r_) : p(p_), it(at), r(r_) {}
+  __device__ __forceinline__ Walker(const AttnParams& p_, const Start& at, int64_t u0) : p(p_), r(at.r) {
     const int lane = (int)threadIdx.x & 31;
-    it.b = sh.b;
-    r = request_of(p, it.b);
-    int64_t rem = u0 - sh.base;
-    it.hv = (int32_t)div_nn(rem, sh.per_head);
-    rem -= it.hv * sh.per_head;
+    it.b = at.b;
+    int64_t rem = u0 - at.base;
+    it.hv = (int32_t)div_nn(rem, at.per_head);
+    rem -= it.hv * at.per_head;
     int64_t s = u0 - rem;  // the head's first unit
     const int32_t tiles = tiles_of(p, r.n);
     for (int32_t t0 = 0;; t0 += 32) {  // 32 tiles at a time: the one that holds the unit
@@ -262,9 +322,19 @@ struct Walker {
     }
     set();
     it.s0 = it.s1;
-    it.s1 += units_of(it.keys);
+    it.s1 += item_units(p, it.keys);
   }
 };
+
+// Whether the CTA has work at all, and `it` moved to its first item.
+// (Its callers have units, s.u0 < s.u1.)
+template <typename Next>
+__device__ __forceinline__ bool first_part(const AttnParams& p, const Schedule& s, Item& it, const Next& next) {
+  if (s.u0 < it.s1 - p.item_cost) return true;
+  if (it.s1 >= s.u1) return false;
+  next(it);
+  return true;
+}
 
 // Bounded wait on an mbarrier phase; false on a time-out (fault bit 3).
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort_flag,

@@ -46,6 +46,7 @@ namespace {
 
 constexpr int kSlice = 16;       // keys a stage: one k-step of the second product
 constexpr float kRaise = 8.0f;
+constexpr int kItemCost = 2;     // units an item costs behind those of its keys
 
 constexpr int kConsumers = kUnit / kSlice;  // warps; a slice of each unit each
 constexpr int kNC = 32 * kConsumers;
@@ -156,16 +157,6 @@ __device__ __forceinline__ Item selected_item(const AttnParams& p, int64_t u, in
   return it;
 }
 
-// What the consumers need of an item, from the producers.
-struct ItemInfo {
-  int32_t ua, uz;      // units [ua, uz) of the item are this CTA's
-  int32_t gs, head0;   // query heads of its virtual head
-  int32_t row0, n;     // rows of q
-  int32_t pos0, keys;
-  int32_t c0, c1;      // the CTAs it lies in
-  int32_t last;        // of this CTA
-};
-
 template <bool F16, int D, int MT, bool SEL>
 __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const AttnParams p) {
   using L = Layout<D, MT>;
@@ -203,16 +194,30 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
   // ---- the CTA's share of the units
   const int32_t list_len = SEL ? p.num_selected * p.ratio + p.local_tokens : 0;
   const int32_t sel_end = SEL ? p.num_selected * p.ratio : 0;
-  const int32_t sel_units = SEL ? units_of(list_len) : 0;
+  const int32_t sel_units = SEL ? item_units(p, list_len) : 0;
   Schedule s;
+  Start at;
   if (SEL) {
     const int64_t rows = min(max(p.query_start[p.num_requests], 0), p.num_tokens);
-    s.share_out(rows * p.hv * sel_units, p.min_units);
+    s.share_out(rows * p.hv * sel_units, p.min_shift);
     __syncthreads();
   } else {
-    s = make_schedule<kNT>(p, sched_sh);
+    s = make_schedule<kNT>(p, sched_sh, at);
   }
   if (s.u0 >= s.u1) return;
+  auto next = [&](Item& it) {
+    if (SEL) {
+      it = selected_item(p, it.s1, sel_units, it.b);
+    } else {
+      Walker w(p, it);
+      w.next();
+      it = w.it;
+    }
+  };
+  Item it;
+  if (SEL) it = selected_item(p, s.u0, sel_units, 0);
+  else it = Walker(p, at, s.u0).it;
+  if (!first_part(p, s, it, next)) return;
   // Registers: 512 threads of 128 at launch, 256 * 72 + 256 * 176 are less; or
   // 384 of 168, of which 128 * 88 + 256 * 208 is the same sum.
   if (warp >= kConsumers) {
@@ -225,11 +230,9 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
     constexpr int kStep = kOwn ? 2 : 1;  // units an iteration
     uint32_t n = 0;                      // slices filled, of any of its consumers
     bool ok = true;
-    Item it;
-    if (SEL) it = selected_item(p, s.u0, sel_units, 0);
-    else it = Walker(p, sched_sh, s.u0).it;
     for (uint32_t k = 0; ok; ++k) {
-      const int ua = (int)(max(s.u0, it.s0) - it.s0), uz = (int)(min(s.u1, it.s1) - it.s0);
+      const Part part(p, s, it);
+      const int ua = part.a, uz = part.z;
       const int kvh = p.splits == 1 ? it.hv : it.hv / p.splits;
       const int sub0 = (it.hv - kvh * p.splits) * p.sub;
       const int gs = min(p.sub, p.group - sub0), head0 = kvh * p.group + sub0;
@@ -282,16 +285,16 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
       copies_arrive(&q_full[k & 1]);
       if (pw == 0 && lane == 0) {
         ItemInfo* o = reinterpret_cast<ItemInfo*>(smem + L::items + (k & 1) * 48);
-        o->ua = ua;
-        o->uz = uz;
+        o->a = ua;
+        o->z = uz;
         o->gs = gs;
         o->head0 = head0;
         o->row0 = it.row0;
         o->n = it.n;
         o->pos0 = it.pos0;
         o->keys = it.keys;
-        o->c0 = it.s0 >= s.u0 ? (int)blockIdx.x : s.owner(it.s0);
-        o->c1 = it.s1 <= s.u1 ? (int)blockIdx.x : s.owner(it.s1 - 1);
+        o->c0 = first_cta(s, it);
+        o->c1 = last_cta(p, s, it);
         o->last = it.s1 >= s.u1;
         ptx::mbar_arrive(&q_full[k & 1]);
       }
@@ -346,13 +349,7 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
         }
       }
       if (!ok || it.s1 >= s.u1) break;
-      if (SEL) {
-        it = selected_item(p, it.s1, sel_units, it.b);
-      } else {
-        Walker w(p, it);
-        w.next();
-        it = w.it;
-      }
+      next(it);
     }
     copies_drain();
   } else {
@@ -367,9 +364,9 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
     for (uint32_t k = 0;; ++k) {
       if (ok) ok = __all_sync(0xffffffffu, wait_phase(&q_full[k & 1], (k >> 1) & 1u, abort_flag, p.fault));
       if (consumers_any(!ok)) break;  // together: the item will not come
-      const ItemInfo it = *reinterpret_cast<const ItemInfo*>(smem + L::items + (k & 1) * 48);
-      const int gs = it.gs, head0 = it.head0, live = it.n * it.gs;
-      const int64_t row0 = it.row0;
+      const ItemInfo info = *reinterpret_cast<const ItemInfo*>(smem + L::items + (k & 1) * 48);
+      const int gs = info.gs, head0 = info.head0, live = info.n * info.gs;
+      const int64_t row0 = info.row0;
       const uint32_t q_addr = ptx::smem_u32(smem + L::q) + (k & 1) * L::kQ + (lane & 15) * L::kRow +
                               (lane >> 4) * 16;  // row, 8-element half
       uint32_t qf[MT == 1 ? D / 16 : 1][4];
@@ -382,8 +379,8 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          lim[mt][h] = min(max(it.pos0 + 1 + (mt * 16 + h * 8 + (lane >> 2)) / gs, 0), it.keys);
-      const int32_t all_see = min(max(it.pos0 + 1, 0), it.keys);
+          lim[mt][h] = min(max(info.pos0 + 1 + (mt * 16 + h * 8 + (lane >> 2)) / gs, 0), info.keys);
+      const int32_t all_see = min(max(info.pos0 + 1, 0), info.keys);
 
       float o[MT][D / 8][4], m[MT][2], l[MT][2];
 #pragma unroll
@@ -396,7 +393,7 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
         l[mt][0] = l[mt][1] = 0.0f;
       }
 
-      for (int j = it.ua; j < it.uz; ++j, ++used) {
+      for (int j = info.a; j < info.z; ++j, ++used) {
         const uint32_t st = used % kStages;
         if (ok) ok = __all_sync(0xffffffffu, wait_phase(&my_full[st], (used / kStages) & 1u, abort_flag, p.fault));
         const uint32_t vm = masks[warp * kStages + st];
@@ -508,13 +505,13 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
         }
         __syncwarp();
         // the last slice's stage stays: the warps join in it
-        if (j + 1 < it.uz && lane == 0) ptx::mbar_arrive(&my_empty[st]);
+        if (j + 1 < info.z && lane == 0) ptx::mbar_arrive(&my_empty[st]);
       }
       if (lane == 0) ptx::mbar_arrive(&q_empty[k & 1]);
 
       // ---- join the warps: their maxima first, then o, each warp's on the common one, 16 rows at a time
       const uint32_t held = (used + kStages - 1) % kStages;
-      const int c = (int)blockIdx.x, c0 = it.c0, c1 = it.c1;
+      const int c = (int)blockIdx.x, c0 = info.c0, c1 = info.c1;
       const bool split = c0 != c1;
       float* part = p.parts + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * part_floats<D, MT>();
 #pragma unroll
@@ -616,7 +613,7 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
           }
         }
       }
-      if (it.last) break;
+      if (info.last) break;
     }
   }
 }
@@ -675,7 +672,8 @@ cudaError_t launch_attn_gather(AttnParams p, const qsa_attn_desc& d, uint8_t* wo
     toks = d.max_new > 0 ? d.max_new : (d.num_tokens + d.num_requests - 1) / d.num_requests;
   const int mt = toks * p.sub <= 16 ? 1 : 2;
   p.tpi = p.num_selected > 0 ? 1 : 16 * mt / p.sub;
-  p.min_units = 1;
+  p.min_shift = 0;
+  p.item_cost = kItemCost;
   p.ratio_shift = -1;
   for (int sh = 0; sh < 31; ++sh)
     if ((1 << sh) == p.ratio) p.ratio_shift = sh;

@@ -34,8 +34,9 @@
 //
 // Schedule: equal shares of the (item, 128-key) units (attn_common.cuh).  Items
 // that lie in several CTAs leave unnormalised parts; a second, small launch
-// joins them with as many CTAs as there are rows to join (one CTA joining the
-// parts of a long item alone would take longer than the item's share).
+// joins them, in the CTAs' order and with as many CTAs as there are parts (one
+// CTA joining the parts of a long item alone would take longer than the item's
+// share).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -52,8 +53,9 @@ namespace {
 
 constexpr int kNT = 384;
 constexpr int kRows = 128;     // query rows a stream
-constexpr int kMetaWords = 8;  // of a split item: parts, first row, tokens, virtual head
+constexpr int kMetaWords = 8;  // of a split item: parts, first row, tokens, first query head
 constexpr float kRaise = 8.0f;
+constexpr int kItemCost = 1;   // units an item costs beside its tiles (start, epilogue)
 
 template <int D>
 struct Geo {
@@ -99,6 +101,103 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// 64 bytes of an output row, in 32-byte stores when rows are aligned to them
+// (a thread writes a row of its own, so a store instruction touches 32 rows,
+// and half as many instructions take half the time).
+__device__ __forceinline__ void store64(uint8_t* dst, const uint32_t (&e)[16], bool by32) {
+  if (by32) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 32 * i), "r"(e[8 * i]),
+                   "r"(e[8 * i + 1]), "r"(e[8 * i + 2]), "r"(e[8 * i + 3]), "r"(e[8 * i + 4]), "r"(e[8 * i + 5]),
+                   "r"(e[8 * i + 6]), "r"(e[8 * i + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4*>(dst + 16 * i) = make_uint4(e[4 * i], e[4 * i + 1], e[4 * i + 2], e[4 * i + 3]);
+  }
+}
+
+// The products of a tile, issued together by one elected lane of the warp.  The
+// MMA warp shares its scheduler with two softmax warps and gets an instruction
+// in some ten cycles, so its loop has few: with an election, 64-bit descriptor
+// sums and a modulo for each MMA the tensor core idled between them (2048 new
+// tokens at 8K: 237 us against 218).
+// S = Q K^T: D / 16 k-steps of 32 bytes, four to a 64-element half; then an
+// arrival on `s_full`, and on `empty` when `last`.  Descriptors: low words of Q
+// and K, and the high word they share.
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc,
+                                         uint64_t* s_full, uint64_t* empty, bool last) {
+  static_assert(kRows * 128 / 16 == 1024, "descriptor offset of a half");
+  if constexpr (D == 128)
+    asm volatile(
+        "{\n .reg .pred e, t, f, q;\n .reg .b64 a, b;\n .reg .b32 la, lb;\n elect.sync _|e, 0xffffffff;\n"
+        " setp.eq.u32 t, 0, 0;\n setp.ne.u32 f, 0, 0;\n setp.ne.and.u32 q, %7, 0, e;\n"
+        " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %2};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, f;\n"
+        " add.u32 la, %1, 2;\n add.u32 lb, %3, 2;\n mov.b64 a, {la, %2};\n mov.b64 b, {lb, %2};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+        " add.u32 la, %1, 4;\n add.u32 lb, %3, 4;\n mov.b64 a, {la, %2};\n mov.b64 b, {lb, %2};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+        " add.u32 la, %1, 6;\n add.u32 lb, %3, 6;\n mov.b64 a, {la, %2};\n mov.b64 b, {lb, %2};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+        " add.u32 la, %1, 1024;\n add.u32 lb, %3, 1024;\n mov.b64 a, {la, %2};\n mov.b64 b, {lb, %2};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+        " add.u32 la, %1, 1026;\n add.u32 lb, %3, 1026;\n mov.b64 a, {la, %2};\n mov.b64 b, {lb, %2};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+        " add.u32 la, %1, 1028;\n add.u32 lb, %3, 1028;\n mov.b64 a, {la, %2};\n mov.b64 b, {lb, %2};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+        " add.u32 la, %1, 1030;\n add.u32 lb, %3, 1030;\n mov.b64 a, {la, %2};\n mov.b64 b, {lb, %2};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n}\n" ::"r"(d), "r"(a), "r"(hi), "r"(b), "r"(idesc), "r"(ptx::smem_u32(s_full)), "r"(ptx::smem_u32(empty)),
+        "r"((uint32_t)last)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred e, t, f, q;\n .reg .b64 a, b;\n .reg .b32 la, lb;\n elect.sync _|e, 0xffffffff;\n"
+        " setp.eq.u32 t, 0, 0;\n setp.ne.u32 f, 0, 0;\n setp.ne.and.u32 q, %7, 0, e;\n"
+        " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %2};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, f;\n"
+        " add.u32 la, %1, 2;\n add.u32 lb, %3, 2;\n mov.b64 a, {la, %2};\n mov.b64 b, {lb, %2};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+        " add.u32 la, %1, 4;\n add.u32 lb, %3, 4;\n mov.b64 a, {la, %2};\n mov.b64 b, {lb, %2};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+        " add.u32 la, %1, 6;\n add.u32 lb, %3, 6;\n mov.b64 a, {la, %2};\n mov.b64 b, {lb, %2};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n}\n" ::"r"(d), "r"(a), "r"(hi), "r"(b), "r"(idesc), "r"(ptx::smem_u32(s_full)), "r"(ptx::smem_u32(empty)),
+        "r"((uint32_t)last)
+        : "memory");
+}
+// O (+)= P V over 128 keys: 8 k-steps of 8 TMEM columns of P and 16 value rows.
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred e, p, t;\n .reg .b64 b;\n .reg .b32 la, lb;\n elect.sync _|e, 0xffffffff;\n"
+      " setp.ne.b32 p, %5, 0;\n setp.eq.u32 t, 0, 0;\n"
+      " mov.b32 la, %1;\n mov.b64 b, {%2, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [la], b, %4, p;\n"
+      " add.u32 la, %1, 8;\n add.u32 lb, %2, 128;\n mov.b64 b, {lb, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [la], b, %4, t;\n"
+      " add.u32 la, %1, 16;\n add.u32 lb, %2, 256;\n mov.b64 b, {lb, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [la], b, %4, t;\n"
+      " add.u32 la, %1, 24;\n add.u32 lb, %2, 384;\n mov.b64 b, {lb, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [la], b, %4, t;\n"
+      " add.u32 la, %1, 32;\n add.u32 lb, %2, 512;\n mov.b64 b, {lb, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [la], b, %4, t;\n"
+      " add.u32 la, %1, 40;\n add.u32 lb, %2, 640;\n mov.b64 b, {lb, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [la], b, %4, t;\n"
+      " add.u32 la, %1, 48;\n add.u32 lb, %2, 768;\n mov.b64 b, {lb, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [la], b, %4, t;\n"
+      " add.u32 la, %1, 56;\n add.u32 lb, %2, 896;\n mov.b64 b, {lb, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [la], b, %4, t;\n"
+      "}\n" ::"r"(d), "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 template <bool F16, int D>
 __global__ void __launch_bounds__(kNT, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
@@ -107,13 +206,14 @@ __global__ void __launch_bounds__(kNT, 1)
   constexpr int kStages = G::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ SchedShared sched_sh;
+  __shared__ ItemInfo item_sh[2];  // by turns, from the copying warp
   uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::bars);
   uint64_t* empty = full + kStages;
   uint64_t* s_full = empty + kStages;   // [2] scores of a stream ready
   uint64_t* p_ready = s_full + 2;       // [2] probabilities stored (and O raised)
   uint64_t* o_done = p_ready + 2;       // [2] an item's last product done
-  uint64_t* q_bar = o_done + 2;         // [2] q loaded, q free
+  uint64_t* q_bar = o_done + 2;         // [2] q (and the item's slot) loaded, free
   uint64_t* done = q_bar + 2;           // abort: the MMAs in flight are done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::misc + 4);
@@ -128,7 +228,7 @@ __global__ void __launch_bounds__(kNT, 1)
       ptx::mbar_init(&s_full[i], 1);
       ptx::mbar_init(&p_ready[i], kRows);
       ptx::mbar_init(&o_done[i], 1);
-      ptx::mbar_init(&q_bar[i], 1);
+      ptx::mbar_init(&q_bar[i], i == 0 ? 1 : 1 + 2 * kRows / 32);  // free: the MMAs, the softmax warps
     }
     ptx::mbar_init(done, 1);
     *abort_flag = 0;
@@ -144,7 +244,8 @@ __global__ void __launch_bounds__(kNT, 1)
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   ptx::tc_fence_before();
-  const Schedule s = make_schedule<kNT>(p, sched_sh);  // with CTA barriers
+  Start at;
+  const Schedule s = make_schedule<kNT>(p, sched_sh, at);  // with a CTA barrier
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int tpt = p.tpi / 2;  // tokens a stream
@@ -152,21 +253,40 @@ __global__ void __launch_bounds__(kNT, 1)
   if (threadIdx.x == 0) p.meta[c * kMetaWords] = 0;
 
   // Registers: 384 threads of 168 at launch, of which the first four warps
-  // leave some to the softmax warps (128 * 72 + 256 * 216 is the same sum).
+  // leave some to the softmax warps (128 * 96 + 256 * 200 are less).
   if (s.u0 < s.u1) {
     if (warp == 0) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-      Walker w(p, sched_sh, s.u0);
       // ------------------------------------------------------------ copies
       const int box = min(p.page_tokens, kUnit);
       uint32_t r = 0, items = 0;
       bool ok = true;
-      for (;;) {
-        const Item& it = w.it;
-        const int ua = (int)(max(s.u0, it.s0) - it.s0), uz = (int)(min(s.u1, it.s1) - it.s0);
+      Walker w(p, at, s.u0);
+      const Item& it = w.it;
+      const bool any = first_part(p, s, w.it, [&](Item&) { w.next(); });
+      if (!any && lane == 0) {
+        item_sh[0].a = -1;
+        ptx::mbar_arrive(&q_bar[0]);
+      }
+      if (any) for (;;) {
+        const Part part(p, s, it);
+        const int ua = part.a, uz = part.z;
         const int nst = it.n > tpt ? 2 : 1;
         if (items > 0) ok = __all_sync(0xffffffffu, wait_phase(&q_bar[1], (items - 1) & 1u, abort_flag, p.fault));
         if (!ok) break;
+        if (lane == 0) {
+          ItemInfo& o = item_sh[items & 1];
+          o.a = ua;
+          o.z = uz;
+          o.row0 = it.row0;
+          o.n = it.n;
+          o.pos0 = it.pos0;
+          o.keys = it.keys;
+          o.head0 = it.hv * p.group;
+          o.c0 = first_cta(s, it);
+          o.c1 = last_cta(p, s, it);
+          o.last = it.s1 >= s.u1;
+        }
         ++items;
         if (lane == 0) {
           ptx::mbar_arrive_expect_tx(&q_bar[0], (uint32_t)(nst * G::kHalves * tpt * p.group * 128));
@@ -216,42 +336,47 @@ __global__ void __launch_bounds__(kNT, 1)
       }
     } else if (warp == 1) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-      Walker w(p, sched_sh, s.u0);
       // ------------------------------------------------------------ products
       constexpr uint32_t id_qk = F16 ? ptx::idesc_f16_f32(128, 128) : ptx::idesc_bf16_f32(128, 128);
       constexpr uint32_t id_pv = (F16 ? ptx::idesc_f16_f32(128, D) : ptx::idesc_bf16_f32(128, D)) | ptx::kIdescBMnMajor;
-      const uint32_t q_u32 = ptx::smem_u32(smem + G::q), ring_u32 = ptx::smem_u32(smem + G::ring);
-      uint32_t r = 0, items = 0, tiles[2] = {0, 0};
+      const uint64_t q_desc = ptx::sw128_desc(ptx::smem_u32(smem + G::q));
+      const uint64_t k_desc = ptx::sw128_desc(ptx::smem_u32(smem + G::ring));
+      const uint64_t v_desc = ptx::sw128_mn_desc(ptx::smem_u32(smem + G::ring), kRows * 128);
+      const uint32_t q_lo = (uint32_t)q_desc, k_lo = (uint32_t)k_desc, qk_hi = (uint32_t)(k_desc >> 32);
+      const uint32_t v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32);
+      constexpr uint32_t kTile16 = G::kTile / 16;  // from tile to tile in a descriptor
+      uint32_t stage = 0, phase = 0;               // of the next tile of the ring
+      uint32_t items = 0, turn[2] = {0, 0};
       bool ok = true;
       auto wwait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, wait_phase(bar, parity, abort_flag, p.fault));
+        const bool there = ptx::mbar_try_wait(bar, parity);
+        return __all_sync(0xffffffffu, there) ||
+               __all_sync(0xffffffffu, wait_phase(bar, parity, abort_flag, p.fault));
       };
-      auto qk = [&](int st, int stage) {
-        const uint64_t a = ptx::sw128_desc(q_u32 + st * G::kTile), b = ptx::sw128_desc(ring_u32 + stage * G::kTile);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint64_t o = (uint64_t)(((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4);
-          ptx::mma_bf16_elect(tmem + st * 128, a + o, b + o, id_qk, ks > 0);
-        }
-        ptx::mma_commit_elect(&s_full[st]);
+      auto advance = [&]() {
+        if (++stage == kStages) stage = 0, phase ^= 1u;
       };
-      for (; ok;) {
-        const Item& it = w.it;
-        const int ua = (int)(max(s.u0, it.s0) - it.s0), uz = (int)(min(s.u1, it.s1) - it.s0);
+      for (;;) {
+        ok = wwait(&q_bar[0], items & 1u);
+        const ItemInfo& it = item_sh[items & 1u];
+        if (!ok || it.a < 0) break;
+        const int ua = it.a, uz = it.z, keys = it.keys, last_item = it.last;
         const int nst = it.n > tpt ? 2 : 1;
-        ok = wwait(&q_bar[0], items & 1u) && wwait(&full[r % kStages], (r / kStages) & 1u);
+        ok = wwait(&full[stage], phase);
         if (!ok) break;
         ++items;
         ptx::tc_fence_after();
-        for (int st = 0; st < nst; ++st) qk(st, r % kStages);
-        ptx::mma_commit_elect(&empty[r % kStages]);
-        ++r;
-        for (int j = ua; j < uz && ok; ++j, r += 2) {  // r: the value tile of j; r + 1: the key tile of j + 1
-          const int vst = r % kStages, kst = (r + 1) % kStages;
-          const bool more = j + 1 < uz;
-          ok = wwait(&full[vst], (r / kStages) & 1u);
+        for (int st = 0; st < nst; ++st)
+          issue_qk<D>(tmem + st * 128, q_lo + st * kTile16, k_lo + stage * kTile16, qk_hi, id_qk, &s_full[st],
+                      &empty[stage], st == nst - 1);
+        advance();
+        for (int j = ua; j < uz; ++j) {
+          const uint32_t vst = stage;
+          ok = wwait(&full[vst], phase);
           if (!ok) break;
-          const int valid = max(0, min(kUnit, it.keys - j * kUnit));
+          advance();  // to the key tile of j + 1, if there is one
+          const bool more = j + 1 < uz;
+          const int valid = max(0, min(kUnit, keys - j * kUnit));
           const int steps = (valid + 15) / 16;
           if (valid & 15) {  // zero the value rows between the last key and the product's end
             uint8_t* v = smem + G::ring + vst * G::kTile;
@@ -262,34 +387,40 @@ __global__ void __launch_bounds__(kNT, 1)
             ptx::fence_proxy_async_smem();
             __syncwarp();
           }
-          const uint64_t vd = ptx::sw128_mn_desc(ring_u32 + vst * G::kTile, kRows * 128);
-          for (int st = 0; st < nst; ++st) {
-            ok = wwait(&p_ready[st], tiles[st] & 1u);
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            if (st >= nst) break;
+            const bool last = st == nst - 1;
+            ok = wwait(&p_ready[st], turn[st]);
             if (!ok) break;
-            ++tiles[st];
+            turn[st] ^= 1u;
             ptx::tc_fence_after();
-            for (int ks = 0; ks < steps; ++ks)
-              ptx::mma_bf16_ts_elect(tmem + 256 + st * D, tmem + st * 128 + ks * 8, vd + (uint64_t)(ks * (2048 >> 4)),
-                                     id_pv, j > ua || ks > 0);
+            const uint32_t d_o = tmem + 256 + st * D, a_p = tmem + st * 128, b_v = v_lo + vst * kTile16;
+            if (valid == kUnit) {
+              issue_pv(d_o, a_p, b_v, v_hi, id_pv, (uint32_t)(j > ua));
+            } else {
+              for (int ks = 0; ks < steps; ++ks)
+                ptx::mma_bf16_ts_elect(d_o, a_p + ks * 8, ((uint64_t)v_hi << 32) | (b_v + ks * (2048 >> 4)), id_pv,
+                                       j > ua || ks > 0);
+            }
             if (!more) ptx::mma_commit_elect(&o_done[st]);
-            if (st == nst - 1) ptx::mma_commit_elect(&empty[vst]);
+            if (last) ptx::mma_commit_elect(&empty[vst]);
             if (more) {
               if (st == 0) {
-                ok = wwait(&full[kst], ((r + 1) / kStages) & 1u);
+                ok = wwait(&full[stage], phase);
                 if (!ok) break;
                 ptx::tc_fence_after();
               }
-              qk(st, kst);
-              if (st == nst - 1) ptx::mma_commit_elect(&empty[kst]);
+              issue_qk<D>(tmem + st * 128, q_lo + st * kTile16, k_lo + stage * kTile16, qk_hi, id_qk, &s_full[st],
+                          &empty[stage], last);
             }
           }
+          if (!ok) break;
+          if (more) advance();
         }
-        // the loop left r one past the next key tile: the item's last value tile was r - 2
-        r -= 1;
         if (!ok) break;
         ptx::mma_commit_elect(&q_bar[1]);
-        if (it.s1 >= s.u1) break;
-        w.next();
+        if (last_item) break;
       }
       if (!ok) {
         ptx::mma_commit_elect(done);
@@ -301,7 +432,6 @@ __global__ void __launch_bounds__(kNT, 1)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     } else {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-      Walker w(p, sched_sh, s.u0);
       // ------------------------------------------------------------ softmax and epilogue
       const int st = (warp - 4) >> 2;
       const int row = ((warp & 3) << 5) + lane;
@@ -312,9 +442,13 @@ __global__ void __launch_bounds__(kNT, 1)
       const float raise = kRaise / sc;  // in units of S
       uint32_t tiles = 0, items = 0;
       bool ok = true;
-      for (;;) {
-        const Item& it = w.it;
-        const int ua = (int)(max(s.u0, it.s0) - it.s0), uz = (int)(min(s.u1, it.s1) - it.s0);
+      for (uint32_t k = 0;; ++k) {
+        ok = __all_sync(0xffffffffu, wait_phase(&q_bar[0], k & 1u, abort_flag, p.fault));
+        const ItemInfo& it = item_sh[k & 1u];
+        if (!ok || it.a < 0) break;
+        // Here now: the last item's slot is free, the next item may be loaded into it.
+        if (lane == 0) ptx::mbar_arrive(&q_bar[1]);
+        const int ua = it.a, uz = it.z;
         const int n = min(it.n - st * tpt, tpt);  // tokens of this stream
         if (n > 0) {
           const int tk = row / p.group;
@@ -369,23 +503,28 @@ __global__ void __launch_bounds__(kNT, 1)
             };
             // With the m there is, while the maxima are taken along: that m stands unless a
             // row's maximum passes it by more than 8, seldom after an item's first tiles.
-            float neg = m == -INFINITY ? 0.0f : -m * sc;
-            sum[0] = sum[1] = 0;
-            mask(0);
-            mask(1);
-            if (j > ua) probabilities(0, neg);
-            max_of(0);
-            max_of(1);
-            ptx::tmem_ld_wait();
-            ptx::tmem_ld_done32(x[2]);
-            ptx::tmem_ld_done32(x[3]);
-            mask(2);
-            mask(3);
-            if (j > ua) probabilities(1, neg);
-            max_of(2);
-            max_of(3);
-            const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-            if (__any_sync(0xffffffffu, j == ua || tile_top > m + raise || (m == -INFINITY && tile_top > m))) {
+            // Then the same code runs once more (not a copy of it: the loop shares the
+            // instruction cache with the copy and MMA warps').
+            for (bool again = false;; again = true) {
+              const float neg = m == -INFINITY ? 0.0f : -m * sc;
+              sum[0] = sum[1] = 0;
+              mask(0);
+              mask(1);
+              probabilities(0, neg);
+              max_of(0);
+              max_of(1);
+              ptx::tmem_ld_wait();
+              ptx::tmem_ld_done32(x[2]);
+              ptx::tmem_ld_done32(x[3]);
+              mask(2);
+              mask(3);
+              probabilities(1, neg);
+              max_of(2);
+              max_of(3);
+              const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+              if (again ||
+                  !__any_sync(0xffffffffu, tile_top > m + raise || (m == -INFINITY && tile_top > m)))
+                break;
               const float mn = fmaxf(m, tile_top);
               const float f = mn == -INFINITY ? 1.0f : ex2((m - mn) * sc);
               m = mn;
@@ -402,10 +541,6 @@ __global__ void __launch_bounds__(kNT, 1)
                   ptx::tmem_st32(t_o + q * 32, o);
                 }
               }
-              neg = m == -INFINITY ? 0.0f : -m * sc;
-              sum[0] = sum[1] = 0;
-              probabilities(0, neg);
-              probabilities(1, neg);
             }
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
@@ -418,11 +553,10 @@ __global__ void __launch_bounds__(kNT, 1)
           ++items;
           if (ok) {
             ptx::tc_fence_after();
-            const int c0 = it.s0 >= s.u0 ? c : s.owner(it.s0);
-            const int c1 = it.s1 <= s.u1 ? c : s.owner(it.s1 - 1);
+            const int c0 = it.c0, c1 = it.c1;
             const bool live = tk < n && row < tpt * p.group;
             const int64_t qrow = it.row0 + st * tpt + tk;
-            const int head = it.hv * p.group + (row - tk * p.group);
+            const int head = it.head0 + (row - tk * p.group);
             if (c0 == c1) {
               const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
               uint8_t* dst = p.out + qrow * p.out_token_stride + (int64_t)head * p.out_head_stride;
@@ -431,47 +565,40 @@ __global__ void __launch_bounds__(kNT, 1)
                 uint32_t o[32];
                 ptx::tmem_ld32(t_o + q * 32, o);
                 ptx::tmem_ld_wait();
-                if (live) {
+                ptx::tmem_ld_done32(o);
+                uint32_t e[16];
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    uint32_t e[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                      // a row that sees nothing has l = 0 and its O is 0 * V: written as zero
-                      const float a = __uint_as_float(o[8 * i + 2 * k]) * inv, b = __uint_as_float(o[8 * i + 2 * k + 1]) * inv;
-                      e[k] = pack2<F16>(l == 0.0f ? 0.0f : a, l == 0.0f ? 0.0f : b);
-                    }
-                    *reinterpret_cast<uint4*>(dst + q * 64 + i * 16) = make_uint4(e[0], e[1], e[2], e[3]);
-                  }
-                }
+                for (int i = 0; i < 16; ++i)  // a row that sees nothing: O is 0 * V, or was never written
+                  e[i] = l == 0.0f ? 0u : pack2<F16>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                if (live) store64(dst + q * 64, e, p.out32);
               }
               if (live && p.lse) p.lse[qrow * p.num_q_heads + head] = (m * sc + log2f(l)) * kLn2;
             } else {
-              float* part = p.parts + (((int64_t)c * 2 + (c == c0 ? 1 : 0)) * 2 + st) * part_floats<D>();
+              float* dst = p.parts + (((int64_t)c * 2 + (c == c0 ? 1 : 0)) * 2 + st) * part_floats<D>();
 #pragma unroll 1
               for (int q = 0; q < D / 32; ++q) {
                 uint32_t o[32];
                 ptx::tmem_ld32(t_o + q * 32, o);
                 ptx::tmem_ld_wait();
+                ptx::tmem_ld_done32(o);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  *reinterpret_cast<uint4*>(part + ((q * 8 + i) * kRows + row) * 4) =
+                  *reinterpret_cast<uint4*>(dst + ((q * 8 + i) * kRows + row) * 4) =
                       l == 0.0f ? make_uint4(0, 0, 0, 0) : make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
               }
-              *reinterpret_cast<float2*>(part + kRows * D + 2 * row) = make_float2(m * sc, l);
+              *reinterpret_cast<float2*>(dst + kRows * D + 2 * row) = make_float2(m * sc, l);
               if (c == c0 && st == 0 && row == 0) {
                 int32_t* meta = p.meta + c * kMetaWords;
                 meta[1] = it.row0;
                 meta[2] = it.n;
-                meta[3] = it.hv;
+                meta[3] = it.head0;
                 meta[0] = c1 - c0 + 1;
               }
             }
             ptx::tc_fence_before();  // O read before the next item's products (through p_ready)
           }
         }
-        if (!ok || it.s1 >= s.u1) break;
-        w.next();
+        if (!ok || it.last) break;
       }
     }
   }
@@ -482,49 +609,70 @@ __global__ void __launch_bounds__(kNT, 1)
 }
 
 // Joins the parts of the items that lie in several CTAs: block (c0, stream, 32
-// rows) for the item that begins in CTA c0's share and ends in a later one.
-// Threads: a row each lane, the warps share out the output's float4 columns,
-// so parts are read 512 contiguous bytes a warp.
+// rows) for the item that begins in CTA c0's share and ends in a later one.  A
+// lane is a row and a warp takes every eighth float4 column, so parts are read
+// 512 contiguous bytes a warp; four parts' loads are in flight together, joined
+// with a running maximum.
 template <bool F16, int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int c0 = (int)blockIdx.x, st = (int)blockIdx.y;
-  const int32_t* meta = p.meta + c0 * kMetaWords;
-  const int nf = meta[0];
+  const int4 meta = *reinterpret_cast<const int4*>(p.meta + c0 * kMetaWords);
+  const int nf = meta.x;
   if (nf == 0) return;
   const int tpt = p.tpi / 2;
-  const int n = min(meta[2] - st * tpt, tpt);
+  const int n = min(meta.z - st * tpt, tpt);
   const int row = (int)blockIdx.z * 32 + ((int)threadIdx.x & 31), warp = (int)threadIdx.x >> 5;
   const int tk = row / p.group;
   if (tk >= n) return;
-  const int64_t qrow = meta[1] + st * tpt + tk;
-  const int head = meta[3] * p.group + (row - tk * p.group);
   auto part_of = [&](int f) {
     return p.parts + (((int64_t)(c0 + f) * 2 + (f == 0 ? 1 : 0)) * 2 + st) * part_floats<D>();
   };
+  constexpr int kPer = D / 32;  // float4 columns a thread
+  constexpr int kBatch = 4;
   float M = -INFINITY, L = 0.0f;
-#pragma unroll 4
-  for (int f = 0; f < nf; ++f) M = fmaxf(M, reinterpret_cast<const float2*>(part_of(f) + kRows * D)[row].x);
-  constexpr int kPer = D / 32;  // float4 columns a warp
   float4 acc[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = make_float4(0, 0, 0, 0);
-#pragma unroll 2
-  for (int f = 0; f < nf; ++f) {
-    const float* pf = part_of(f);
-    const float2 e = reinterpret_cast<const float2*>(pf + kRows * D)[row];
-    const float w = e.x == -INFINITY ? 0.0f : ex2(e.x - M);
-    L += e.y * w;
+  for (int f0 = 0; f0 < nf; f0 += kBatch) {
+    float2 e[kBatch];
+    float4 v[kBatch][kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const float4 v = reinterpret_cast<const float4*>(pf)[(warp + 8 * i) * kRows + row];
-      acc[i].x = fmaf(v.x, w, acc[i].x);
-      acc[i].y = fmaf(v.y, w, acc[i].y);
-      acc[i].z = fmaf(v.z, w, acc[i].z);
-      acc[i].w = fmaf(v.w, w, acc[i].w);
+    for (int b = 0; b < kBatch; ++b) {
+      e[b] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[b][i] = make_float4(0, 0, 0, 0);
+      if (f0 + b < nf) {
+        const float* pf = part_of(f0 + b);
+        e[b] = reinterpret_cast<const float2*>(pf + kRows * D)[row];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) v[b][i] = reinterpret_cast<const float4*>(pf)[(warp + 8 * i) * kRows + row];
+      }
+    }
+    float m = M;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) m = fmaxf(m, e[b].x);
+    const float keep = M == -INFINITY ? 0.0f : ex2(M - m);
+    M = m;
+    L *= keep;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = make_float4(acc[i].x * keep, acc[i].y * keep, acc[i].z * keep, acc[i].w * keep);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const float w = e[b].x == -INFINITY ? 0.0f : ex2(e[b].x - M);
+      L += e[b].y * w;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        acc[i].x = fmaf(v[b][i].x, w, acc[i].x);
+        acc[i].y = fmaf(v[b][i].y, w, acc[i].y);
+        acc[i].z = fmaf(v[b][i].z, w, acc[i].z);
+        acc[i].w = fmaf(v[b][i].w, w, acc[i].w);
+      }
     }
   }
+  const int64_t qrow = meta.y + st * tpt + tk;
+  const int head = meta.w + (row - tk * p.group);
   const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
   uint8_t* dst = p.out + qrow * p.out_token_stride + (int64_t)head * p.out_head_stride;
 #pragma unroll
@@ -613,7 +761,9 @@ cudaError_t launch_attn_tile(AttnParams p, const qsa_attn_desc& d, uint8_t* work
   p.hv = d.kv.num_kv_heads;
   const int tpt = kRows / p.group;
   p.tpi = 2 * tpt;
-  p.min_units = 2;
+  p.min_shift = 1;
+  p.item_cost = kItemCost;
+  p.out32 = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.out_token_stride % 32 == 0 && p.out_head_stride % 32 == 0;
   const CUtensorMapDataType ty = f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap qm, km, vm;
   const cuuint32_t es[4] = {1, 1, 1, 1};

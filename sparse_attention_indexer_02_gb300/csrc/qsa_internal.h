@@ -137,7 +137,9 @@ struct AttnParams {
   int32_t group;              // query heads of a key/value head
   int32_t hv, splits, sub;    // virtual heads = kv heads * splits, of `sub` query heads each
   int32_t tpi;                // tokens an item
-  int32_t min_units;          // units a CTA takes at least (fewer CTAs take part then)
+  int32_t item_cost;          // units an item costs behind those of its keys
+  int32_t out32;              // tile form: rows of out are 32-byte aligned
+  int32_t min_shift;          // a CTA takes at least 2^min_shift units (fewer CTAs take part then)
   int32_t num_selected, ratio, ratio_shift, local_tokens;  // ratio_shift: log2, or -1
   int32_t near_rows;          // keys and values: equal strides, offsets below 2^36 bytes
   float scale_log2;           // scale * log2(e)
