@@ -384,6 +384,30 @@ def e4m3_reference(x):
 
 
 @gpu
+def test_store_index_keys_code_borders(cuda):
+    """Rows whose quotients lie on and next to the borders between codes, for
+    scales of every size: each code is the division's."""
+    r = np.random.default_rng(5)
+    grid = np.arange(256, dtype=np.uint8)
+    val = torch.from_numpy(grid).view(torch.float8_e4m3fn).float().numpy()
+    val = np.sort(val[np.isfinite(val)])
+    mids = (val[1:] + val[:-1]) / 2
+    T = 4096
+    amax = torch.from_numpy((r.integers(1, 256, T) * 2.0 ** r.integers(-140, 100, T)).astype(np.float32)).bfloat16().float()
+    near = torch.from_numpy(r.choice(mids, (T, 128)).astype(np.float32)) * (amax / 448.0)[:, None]
+    bits = near.bfloat16().view(torch.int16) + torch.from_numpy(r.integers(-1, 2, (T, 128)).astype(np.int16))
+    keys = bits.view(torch.bfloat16).float().nan_to_num(0.0).clamp(-amax[:, None], amax[:, None]).bfloat16()
+    keys[:, 0] = amax.bfloat16()
+    cache = torch.zeros((T // 64, 64 * 132), dtype=torch.uint8, device="cuda")
+    torch_api.store_index_keys(keys.cuda(), torch.arange(T, device="cuda"), cache, page_cols=64,
+                               kv_dtype=qsa.KV_FP8_E4M3, scale_offset=64 * 128)
+    codes, scale = e4m3_reference(keys)
+    got = cache.cpu()
+    assert torch.equal(got[:, 64 * 128:].contiguous().view(torch.float32).flatten(), scale)
+    assert torch.equal(got[:, :64 * 128].reshape(T, 128), codes)
+
+
+@gpu
 @pytest.mark.parametrize("T,pc,fp8", [(1, 1, True), (1, 64, False), (100, 4, True), (1001, 64, True), (77, 16, False),
                                       (513, 20, True), (64, 3, True)])
 def test_store_index_keys(cuda, T, pc, fp8):
