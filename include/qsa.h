@@ -603,7 +603,7 @@ qsa_status qsa_paged_attention(const qsa_attn_desc* desc, const void* q, const v
 qsa_status qsa_paged_attention_workspace(const qsa_attn_desc* desc, size_t* bytes);
 
 /* The form qsa_paged_attention takes for `desc` (host only): tiles when a
- * request may bring more than 32 query rows a key/value head, no columns are
+ * request may bring more than 16 query rows a key/value head, no columns are
  * selected and pages hold 8, 16, 32, 64 or a multiple of 128 tokens; else
  * gathered rows. */
 qsa_status qsa_plan_attention(const qsa_attn_desc* desc, int32_t* form);

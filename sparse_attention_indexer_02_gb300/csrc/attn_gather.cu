@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
       auto col_of = [&](int32_t at) -> int32_t { return p.ratio_shift >= 0 ? at >> p.ratio_shift : at / p.ratio; };
       auto entry_of = [&](int j) -> int32_t {  // SEL: the column listed for the place, -1 none
         const int32_t at = place_of(j);
-        return in_share(j) && at < sel_end ? __ldg(sel + col_of(at)) : -1;
+        return in_share(j) && at < sel_end ? sel[col_of(at)] : -1;
       };
       auto token_of = [&](int j, int32_t col) -> int32_t {  // the token of the place, -1 none
         const int32_t at = place_of(j);
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
         return t < keys ? (int32_t)t : -1;
       };
       auto page_of = [&](int32_t tok) -> int32_t {
-        return tok < 0 ? 0 : __ldg(table + (p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_tokens));
+        return tok < 0 ? 0 : table[p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_tokens];
       };
       int32_t tok = token_of(ua, SEL ? entry_of(ua) : 0), page = page_of(tok);
       int32_t col2 = SEL ? entry_of(ua + kStep) : 0;
@@ -524,12 +524,16 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
           if ((lane & 3) == 0) ml[warp * kRows + mt * 16 + h * 8 + (lane >> 2)] = make_float2(m[mt][h], t);
         }
       consumers_sync();
-      auto write_out = [&](int r, int d, float M, float Lsum, const float (&acc)[4]) {
+      auto write_out = [&](int r, int d, float M, float Lsum, const auto& acc) {
         const int tk = r / gs, g = r - tk * gs;
         const int64_t row = row0 + tk;
         const float inv = Lsum > 0.0f ? 1.0f / Lsum : (Lsum == 0.0f ? 0.0f : Lsum);
-        uint2 w = make_uint2(pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv));
-        *reinterpret_cast<uint2*>(p.out + row * p.out_token_stride + (int64_t)(head0 + g) * p.out_head_stride + d * 2) = w;
+        uint8_t* dst = p.out + row * p.out_token_stride + (int64_t)(head0 + g) * p.out_head_stride + d * 2;
+        if constexpr (sizeof(acc) == 16)
+          *reinterpret_cast<uint2*>(dst) =
+              make_uint2(pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv));
+        else
+          *reinterpret_cast<uint32_t*>(dst) = pack2<F16>(acc[0] * inv, acc[1] * inv);
         if (d == 0 && p.lse) p.lse[row * p.num_q_heads + head0 + g] = (M + log2f(Lsum)) * kLn2;
       };
 #pragma unroll
@@ -589,27 +593,76 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
         }
         consumers_sync();
         if (last_sh) {
-          auto part_of = [&](int f) { return p.parts + ((int64_t)f * 2 + (f == c0 ? 1 : 0)) * part_floats<D, MT>(); };
-          for (int i = tid; i < live * (D / 4); i += kNC) {
-            const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
-            float M = -INFINITY;
-#pragma unroll 4
-            for (int f = c0; f <= c1; ++f)
-              M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(part_of(f) + kRows * D + 2 * r)).x);
-            float Ls = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-            for (int f = c0; f <= c1; ++f) {
-              const float* pf = part_of(f);
-              const float2 e = __ldcg(reinterpret_cast<const float2*>(pf + kRows * D + 2 * r));
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(pf + r * D + d));
-              const float x = e.x == -INFINITY ? 0.0f : ex2(e.x - M);
-              Ls += e.y * x;
-              acc[0] = fmaf(v.x, x, acc[0]);
-              acc[1] = fmaf(v.y, x, acc[1]);
-              acc[2] = fmaf(v.z, x, acc[2]);
-              acc[3] = fmaf(v.w, x, acc[3]);
+          // A warp takes two rows at a time, a lane kPer columns of each; the lanes hold
+          // the parts' weights.  Eight parts of both rows are in flight together: the
+          // parts of a long request with one key/value head are 600 KB, read by this CTA
+          // alone (a thread a column, four parts at a time: 115 us at 30000 keys of one
+          // head and 32 rows; so: 50).
+          constexpr int kPer = D / 32, kHold = (kMaxGrid + 31) / 32;
+          const int n = c1 - c0 + 1;
+          auto part_of = [&](int f) {
+            return p.parts + ((int64_t)(c0 + f) * 2 + (f == 0 ? 1 : 0)) * part_floats<D, MT>();
+          };
+          for (int r0 = warp; r0 < live; r0 += 2 * kConsumers) {
+            float2 e[2][kHold];
+            float M[2] = {-INFINITY, -INFINITY}, Ls[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < kHold; ++k)
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                const int f = k * 32 + lane, r = r0 + t * kConsumers;
+                e[t][k] = make_float2(-INFINITY, 0.0f);
+                if (f < n && r < live)
+                  e[t][k] = __ldcg(reinterpret_cast<const float2*>(part_of(f) + kRows * D + 2 * r));
+              }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+              for (int k = 0; k < kHold; ++k) M[t] = fmaxf(M[t], e[t][k].x);
+#pragma unroll
+              for (int o = 16; o >= 1; o >>= 1) M[t] = fmaxf(M[t], __shfl_xor_sync(0xffffffffu, M[t], o));
+#pragma unroll
+              for (int k = 0; k < kHold; ++k) {
+                e[t][k].x = e[t][k].x == -INFINITY ? 0.0f : ex2(e[t][k].x - M[t]);  // the weight now
+                Ls[t] += e[t][k].y * e[t][k].x;
+              }
+#pragma unroll
+              for (int o = 16; o >= 1; o >>= 1) Ls[t] += __shfl_xor_sync(0xffffffffu, Ls[t], o);
             }
-            write_out(r, d, M, Ls, acc);
+            float acc[2][kPer] = {};
+            const bool two = r0 + kConsumers < live;
+#pragma unroll
+            for (int k = 0; k < kHold; ++k) {
+              for (int f0 = k * 32; f0 < min(n, (k + 1) * 32); f0 += 8) {
+                float v[2][8][kPer];
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+#pragma unroll
+                  for (int t = 0; t < 2; ++t) {
+                    const bool there = f0 + b < n && (t == 0 || two);
+                    const float* src = part_of(there ? f0 + b : 0) + (r0 + (there ? t : 0) * kConsumers) * D + lane * kPer;
+                    if constexpr (kPer == 4) {
+                      const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+                      v[t][b][0] = x.x, v[t][b][1] = x.y, v[t][b][2] = x.z, v[t][b][3] = x.w;
+                    } else {
+                      const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+                      v[t][b][0] = x.x, v[t][b][1] = x.y;
+                    }
+                  }
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+#pragma unroll
+                  for (int t = 0; t < 2; ++t) {
+                    const float w = __shfl_sync(0xffffffffu, e[t][k].x, (f0 + b) & 31);
+#pragma unroll
+                    for (int c2 = 0; c2 < kPer; ++c2)
+                      acc[t][c2] = f0 + b < n ? fmaf(v[t][b][c2], w, acc[t][c2]) : acc[t][c2];
+                  }
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              if (t == 0 || two) write_out(r0 + t * kConsumers, lane * kPer, M[t], Ls[t], acc[t]);
           }
         }
       }

@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kNT, 1)
         const int32_t* table = p.block_table + (int64_t)it.b * p.table_stride;
         auto page_at = [&](int j) -> int32_t {  // the page of the lane's box of key tile j
           const int32_t t = j * kUnit + lane * box;
-          return j < uz && lane * box < kUnit && t < it.keys ? __ldg(table + t / p.page_tokens) : 0;
+          return j < uz && lane * box < kUnit && t < it.keys ? table[t / p.page_tokens] : 0;
         };
         int32_t page = page_at(ua);
         for (int j = ua; j < uz && ok; ++j) {

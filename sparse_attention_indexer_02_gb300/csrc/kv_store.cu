@@ -12,6 +12,16 @@
 namespace qsa {
 namespace {
 
+// 16 bytes past L1.  Not through the read-only path: a launch may begin while
+// the kernel that writes the rows still runs.
+__device__ __forceinline__ uint4 ld_rows_v4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
 // ---- keys and values --------------------------------------------------------
 // A row of a token is num_kv_heads * head_dim / 8 chunks of 16 bytes, for the
 // key and for the value.  The chunks of all tokens are numbered through, and a
@@ -44,8 +54,8 @@ __global__ void __launch_bounds__(kNT) store_kv_kernel(const StoreKvParams p) {
     const int64_t s = p.slots[t];
     if (s < 0 || s >= p.num_slots) continue;
     slot[u] = s;
-    kv[u] = ld_stream_v4(p.k + t * p.k_row_stride + head[u] * p.k_row_head_stride + chunk[u] * 16);
-    vv[u] = ld_stream_v4(p.v + t * p.v_row_stride + head[u] * p.v_row_head_stride + chunk[u] * 16);
+    kv[u] = ld_rows_v4(p.k + t * p.k_row_stride + head[u] * p.k_row_head_stride + chunk[u] * 16);
+    vv[u] = ld_rows_v4(p.v + t * p.v_row_stride + head[u] * p.v_row_head_stride + chunk[u] * 16);
   }
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
@@ -85,7 +95,7 @@ __global__ void __launch_bounds__(kIdxNT) store_index_kernel(const StoreIndexPar
   const bool live = s >= 0 && s < p.num_slots;
   if (__ballot_sync(0xffffffffu, live) == 0) return;
   uint4 w = make_uint4(0, 0, 0, 0);
-  if (live) w = ld_stream_v4(p.keys + t * p.row_stride + l * 16);
+  if (live) w = ld_rows_v4(p.keys + t * p.row_stride + l * 16);
   const int64_t pg = live ? s / p.page_cols : 0, j = live ? s - pg * p.page_cols : 0;
   if (!p.fp8) {
     if (live) *reinterpret_cast<uint4*>(p.cache + pg * p.key_page_stride + j * 256 + l * 16) = w;

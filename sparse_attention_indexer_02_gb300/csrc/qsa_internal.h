@@ -145,8 +145,13 @@ struct AttnParams {
   float scale_log2;           // scale * log2(e)
 };
 constexpr int64_t kMaxKeys = 0x7FFFFC00;  // keys of a request (room for rounding up in 32 bits)
-// Query rows of a key/value head above which a call takes tiles.
-constexpr int kGatherRows = 32;
+constexpr int kGatherRows = 32;  // rows of the gathered form's largest tile
+// Query rows of a key/value head above which a call takes tiles.  At 16 rows
+// the gathered form wins (us, gathered / tiles: 16 requests of 8000 keys 85 /
+// 92, 64 of 1000 51 / 59, one of 1000 9.9 / 11.8, one of 30000 with two heads
+// 21.8 / 25.7), at 20, where it needs a second row tile, it does not (90 / 92,
+// 60 / 59, 13.2 / 12.0; 32 rows: 91 / 93, 63 / 60, 14.2 / 12.4, 35.0 / 29.0).
+constexpr int kTileAbove = 16;
 size_t attn_gather_workspace(int head_dim);
 size_t attn_tile_workspace(int head_dim);
 bool attn_tile_supports(const qsa_attn_desc& d, const char** why);

@@ -77,7 +77,7 @@ qsa_status plan_form(const qsa_attn_desc* d, int32_t* form) {
   int64_t toks = d->max_new;
   if (toks == 0 && d->num_requests > 0) toks = (d->num_tokens + d->num_requests - 1) / d->num_requests;
   const int64_t rows = toks * (d->num_q_heads / d->kv.num_kv_heads);
-  *form = tile && rows > qsa::kGatherRows ? QSA_ATTN_TILE : QSA_ATTN_GATHER;
+  *form = tile && rows > qsa::kTileAbove ? QSA_ATTN_TILE : QSA_ATTN_GATHER;
   return QSA_OK;
 }
 

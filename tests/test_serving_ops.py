@@ -179,10 +179,10 @@ def test_empty_calls_launch_nothing(lib):
 
 
 def test_attention_form_choice(lib):
-    """Tiles above 32 query rows a key/value head (here 4 a token), where pages allow them."""
+    """Tiles above 16 query rows a key/value head (here 4 a token), where pages allow them."""
     plan = lambda **kw: qsa.plan_attention(_attn_desc(**kw))  # noqa: E731
-    assert plan(max_new=8) == _abi.ATTN_GATHER and plan(max_new=9) == _abi.ATTN_TILE
-    assert plan(max_new=0, num_tokens=16) == _abi.ATTN_GATHER and plan(max_new=0, num_tokens=17) == _abi.ATTN_TILE
+    assert plan(max_new=4) == _abi.ATTN_GATHER and plan(max_new=5) == _abi.ATTN_TILE
+    assert plan(max_new=0, num_tokens=8) == _abi.ATTN_GATHER and plan(max_new=0, num_tokens=9) == _abi.ATTN_TILE
     for pt, form in ((8, 2), (16, 2), (32, 2), (64, 2), (128, 2), (256, 2), (384, 2), (1, 1), (20, 1), (192, 1)):
         assert plan(max_new=64, kv=_kv_desc(page_tokens=pt)) == form, pt
     assert plan(max_new=64, num_selected=8) == _abi.ATTN_GATHER
@@ -602,6 +602,58 @@ def test_attention_rows_that_see_nothing(cuda, form):
 
 @gpu
 @pytest.mark.parametrize("form", [_abi.ATTN_GATHER, _abi.ATTN_TILE], ids=["gather", "tile"])
+@pytest.mark.parametrize("B", [33, 390, 1100])
+def test_attention_many_requests(cuda, form, B):
+    """More requests than a warp, than a CTA, than two rounds of a CTA, some without new tokens."""
+    r = np.random.default_rng(B)
+    lens = [(int(s), min(int(s), int(n))) for s, n in zip(r.integers(0, 200, B), r.integers(0, 4, B))]
+    pr = Problem(lens, 1, 2, 64, 16, "bf16", seed=B)
+    out, lse = pr.run(form=form)
+    pr.check(out, lse)
+
+
+@gpu
+@pytest.mark.parametrize("form", [_abi.ATTN_GATHER, _abi.ATTN_TILE], ids=["gather", "tile"])
+def test_attention_metadata_out_of_range(cuda, form):
+    """Page ids are clamped into the pool, lengths to what the table holds, row
+    starts to the rows there are: the results are those of the clamped values."""
+    pr = Problem([(300, 40), (64, 3)], 2, 4, 128, 32, "bf16", seed=21)
+    pr.kc.nan_to_num_(0.5)
+    pr.vc.nan_to_num_(0.5)
+    pages = pr.kc.shape[0]
+    good = pr.table.clone()
+    good[0, 1], good[0, 2], good[1, 0] = 0, pages - 1, pages - 1
+    bad = good.clone()
+    bad[0, 1], bad[0, 2], bad[1, 0] = -7, 2**31 - 1, pages
+    pr.table = good
+    want = pr.run(form=form)
+    pr.table = bad
+    got = pr.run(form=form)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # more tokens than the table's 32 * 12 hold: the keys end there, positions do not
+    pr.table = good
+    cap = good.shape[1] * 32
+    for n in (cap + 40, 2**31 - 1):
+        pr.seq = _cu([n, 64])
+        far = pr.run(form=form)
+        pr.seq = _cu([cap + 40, 64])
+        near = pr.run(form=form)
+        assert torch.equal(far[0], near[0]) and not far[0].isnan().any()
+    pr.seq = _cu([-5, 64])
+    neg = pr.run(form=form)
+    assert (neg[1][:40] == -math.inf).all() and (neg[0][:40] == 0).all()
+    pr.seq = _cu([300, 64])
+    pr.start = _cu([0, 40, 10**6])
+    late = pr.run(form=form)
+    assert torch.equal(late[0], want[0])
+    pr.start = _cu([-3, 40, 20])   # decreasing: the second request has no rows
+    out = torch.full_like(want[0], 7.0)
+    pr.run(form=form, out=out)
+    assert torch.equal(out[:40], want[0][:40]) and (out[40:] == 7).all()
+
+
+@gpu
+@pytest.mark.parametrize("form", [_abi.ATTN_GATHER, _abi.ATTN_TILE], ids=["gather", "tile"])
 def test_attention_large_scores(cuda, form):
     """Scores of hundreds: one key takes all; growing maxima along the keys raise m again and again."""
     pr = Problem([(1500, 40)], 1, 4, 128, 64, "bf16", seed=3, spread=30.0)
@@ -614,10 +666,14 @@ def test_attention_large_scores(cuda, form):
 
 
 @gpu
-@pytest.mark.parametrize("form,lens", [(_abi.ATTN_GATHER, [(40000, 1), (3, 1)]), (_abi.ATTN_TILE, [(30000, 100)])])
-def test_attention_splits_join_the_same_way(cuda, form, lens):
-    """Long keys over many CTAs: right, the same bits each time, and the counters zero again."""
-    pr = Problem(lens, 2, 4, 128, 64, "bf16", seed=5)
+@pytest.mark.parametrize("form,lens,hkv,group,D", [
+    (_abi.ATTN_GATHER, [(40000, 1), (3, 1)], 2, 4, 128), (_abi.ATTN_GATHER, [(40000, 1)], 1, 30, 128),
+    (_abi.ATTN_GATHER, [(20000, 3)], 1, 9, 64), (_abi.ATTN_TILE, [(30000, 100)], 2, 4, 128),
+    (_abi.ATTN_TILE, [(25000, 3)], 1, 11, 64)])
+def test_attention_splits_join_the_same_way(cuda, form, lens, hkv, group, D):
+    """Long keys over many CTAs, all of them for the cases of one key/value
+    head: right, the same bits each time, and the counters zero again."""
+    pr = Problem(lens, hkv, group, D, 64, "bf16", seed=5)
     ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
     first = pr.run(form=form, workspace=ws)
     pr.check(*first)
