@@ -9,32 +9,33 @@
 // and over CTAs.
 //
 // What bounds it is the key/value bytes: HBM for a decode step, whose 16 or 32
-// query rows do at most 32 flop a byte, L2 for chunks of selected rows.  So
-// the kernel is a stream first.  Eight consumer warps work on 16 keys each of
-// a 128-key unit, every one alone, with a ring of kStages 16-key stages of its
-// own; four producer warps fill the rings, two consumers' each, 32 rows at a
-// time: a lane works out where its row lies (list entry, token, page: loaded
-// ahead) and the warp copies the rows with 16-byte asynchronous copies, half a
-// warp a row, the row offsets passed round by shuffles.  Producers run ahead
-// into the next items, their q included; consumers meet only to join their
-// parts at the end of an item.  (With the copies issued by the consuming warps
-// themselves a slice was one chain of copies, products and softmax steps,
-// 2000 cycles and more whatever the memory did: 178 us for 512 selected rows
-// of 2148 keys.)
+// query rows do at most 32 flop a byte (9 requests x 4 rows at 64-128K tokens:
+// 486 us, 7.1 TB/s), random 256-byte rows of HBM for selected decode (16 x 8256
+// keys: 50 us, of which copies alone are 49), the consumers' chain of steps for
+// selected chunks, whose rows come from L2 (512 rows x 2148 keys: 117 us; copies
+// alone 81).  So the kernel is a stream first.  Eight consumer warps work on 16
+// keys each of a 128-key unit, every one alone, with a ring of kStages 16-key
+// stages of its own; producer warps fill the rings, 32 rows at a time: a lane
+// works out where its row lies (list entry, token, page: loaded ahead) and the
+// warp copies the rows with 16-byte asynchronous copies, half a warp a row, the
+// row offsets passed round by shuffles.  Producers run ahead into the next
+// items, their q included; consumers meet only to join their parts at the end
+// of an item.  (With the copies issued by the consuming warps themselves a slice
+// was one chain of copies, products and softmax steps, 2000 cycles and more
+// whatever the memory did: 178 us for those 512 selected rows.)
 //
 // Rows may lie anywhere, so pages of any size, any cache strides and selected
 // columns are one path; rows that are not seen are filled with zeros by the
 // same instruction (source size 0), so that nothing a cache holds elsewhere can
 // enter a product.  Rows are 16 bytes apart more than their length, which keeps
-// the matrix loads free of bank conflicts.  Up to 200 KB of copies in flight
-// on each SM cover the latency.
+// the matrix loads free of bank conflicts.
 //
 // The products are mma.sync (m16n8k16): with at most 32 query rows a tcgen05
 // tile of 128 rows would be three quarters padding, and the stream leaves the
 // tensor cores idle most of the time either way.  The probabilities go from
 // the accumulator layout of the first product straight into the operand layout
-// of the second, in registers, rounded to the 16-bit type there (relative
-// 2^-9 or 2^-12 a term; their sum is taken from the fp32 values).
+// of the second, in registers, rounded to the 16-bit type there (by at most
+// 2^-8 or 2^-11 of a term; their sum is taken from the fp32 values).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -50,6 +51,8 @@ constexpr int kItemCost = 2;     // units an item costs behind those of its keys
 
 constexpr int kConsumers = kUnit / kSlice;  // warps; a slice of each unit each
 constexpr int kNC = 32 * kConsumers;
+// Two stages, 136 KB of copies in flight on an SM, leave L1 92 KB to land them
+// through; three leave it 28 KB (the 9 x 4 rows: 503 us against 620).
 constexpr int kStages = 2;
 
 // Producer warps and the register split.  A warp issues one copy instruction

@@ -42,14 +42,29 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "attn_common.cuh"
+#include "attn_ptx.cuh"
 
 namespace qsa {
-namespace umma {
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // umma.cu
-}
 namespace attn {
 namespace {
+
+// The driver's tensor-map encoder (looked up once), or null.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
 
 constexpr int kNT = 384;
 constexpr int kRows = 128;     // query rows a stream
@@ -747,7 +762,7 @@ size_t attn_tile_workspace(int head_dim) {
 
 cudaError_t launch_attn_tile(AttnParams p, const qsa_attn_desc& d, uint8_t* workspace, cudaStream_t stream,
                              const char** msg) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = umma::tensor_map_encoder();
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) {
     *msg = "cuTensorMapEncodeTiled is unavailable from the driver";
     return cudaErrorInvalidValue;

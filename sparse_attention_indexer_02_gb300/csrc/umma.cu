@@ -16,8 +16,10 @@ namespace umma {
 
 __device__ unsigned int g_fault_word = 0;
 
-// The driver's tensor-map encoder (looked up once), or null; also used by attn_tile.cu.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+namespace {
+
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -30,8 +32,6 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   });
   return fn;
 }
-
-namespace {
 
 int pick_n(int rows_per_group, int heads) {
   const int need = rows_per_group * heads;
@@ -167,7 +167,7 @@ cudaError_t launch_umma(const ScoreParams& p, cudaStream_t stream, const char** 
     if (fuse != nullptr) *msg = "the lean form has no fused selection";
     return cudaErrorInvalidValue;
   }
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) {
     *msg = "cuTensorMapEncodeTiled is unavailable from the driver";
     return cudaErrorInvalidValue;
