@@ -356,10 +356,11 @@ const char* qsa_last_error(void);
  * (its selection for that row is unspecified).  Bit 2: a qsa_page_stream
  * launch gave up waiting for a page (its checksum is unspecified).  Bit 3: a
  * qsa_paged_attention launch gave up waiting for a copy or a product (its
- * output is unspecified).  Synchronises the current device, then writes the word to *flags (host pointer).  When `clear` is
- * non-zero it then clears the word and zeroes the counter array of
- * qsa_paged_mqa_topk_noalloc on the current device (synchronously), so the
- * next no-alloc call starts clean after a failed one.
+ * output is unspecified).  Synchronises the current device, then writes the
+ * word to *flags (host pointer).  When `clear` is non-zero it then clears the
+ * word and zeroes the counter array of qsa_paged_mqa_topk_noalloc on the
+ * current device (synchronously), so the next no-alloc call starts clean after
+ * a failed one.
  */
 qsa_status qsa_device_status(uint32_t* flags, int32_t clear);
 

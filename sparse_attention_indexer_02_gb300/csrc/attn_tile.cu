@@ -13,7 +13,9 @@
 //                shared memory, where its rows are keys: the MN-major operand)
 //
 // TMEM is full: S/P and O of both streams are 2 * 128 + 2 * D columns.
-// What bounds a chunk is the tensor core (4 * D flop a row and key); the
+// What bounds a chunk is the tensor core (4 * D flop a row and key): 8192 new
+// tokens at 32768, 32 heads of 128, take 2080 us, 1850 TFLOP/s, 0.97 of the
+// measured bf16 rate (back to back 2620, under the power limit).  The
 // exponentials are half its time.  The two streams exist to keep it busy: the
 // softmax of one runs while the MMAs of the other do.  Two tiles on one key
 // tile also halve what L2 has to deliver, 64 KB for 2048 cycles of MMA.

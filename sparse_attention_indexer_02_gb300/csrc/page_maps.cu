@@ -10,7 +10,9 @@
 // The tokens' own page lookups never meet a write of the launch: pages a
 // request had before come from the table, new ones straight from the free list.
 //
-// Bound by launch latency at every size that occurs: 28 bytes a token.
+// Bound by latency at every size that occurs (28 bytes a token): the launch, the
+// lengths' load, the scan, a search and a page lookup one after the other; 3.8 us
+// for 16 requests of a token, 5.3 for 512 requests and 33 K tokens.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -153,10 +153,11 @@ at::Tensor slice_of(const at::Tensor& buf, at::ScalarType ty, int64_t at, int64_
 }
 
 // (context_lens, new_lens, free_pages, block_table, page_tokens, max_tokens,
-//  ratio, partial_cols, out: tuple of 8 or None) -> (status, 8 outputs)
+//  ratio, partial_cols, out: PageMaps or None, PageMaps) -> (status, PageMaps)
 PyObject* build_page_maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    arity(n, 9);
+    arity(n, 10);
+    need(PyType_Check(a[9]) && PyType_IsSubtype((PyTypeObject*)a[9], &PyTuple_Type), "the result's type must be a tuple");
     const at::Tensor &ctx = tensor(a[0], "context_lens"), &nw = tensor(a[1], "new_lens"),
                      &fp = tensor(a[2], "free_pages"), &bt = tensor(a[3], "block_table");
     vec(ctx, "context_lens", at::kInt, -1);
@@ -208,10 +209,28 @@ PyObject* build_page_maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
         o[0].data_ptr<int32_t>(), o[1].data_ptr<int32_t>(), o[2].data_ptr<int64_t>(), o[3].data_ptr<int32_t>(),
         o[4].data_ptr<int32_t>(), o[5].data_ptr<int32_t>(), o[6].data_ptr<int64_t>(), o[7].data_ptr<int32_t>(),
         place.stream());
-    PyObject* r = PyTuple_New(9);
-    if (!r) return nullptr;
+    PyObject* maps = a[8];
+    if (given(maps)) {
+      Py_INCREF(maps);
+    } else {
+      // the named tuple from a plain one, as its own _make does
+      PyObject* plain = PyTuple_New(8);
+      if (!plain) return nullptr;
+      for (int i = 0; i < 8; ++i) PyTuple_SET_ITEM(plain, i, wrap(o[i]));
+      PyObject* args = PyTuple_Pack(1, plain);
+      Py_DECREF(plain);
+      if (!args) return nullptr;
+      maps = PyTuple_Type.tp_new((PyTypeObject*)a[9], args, nullptr);
+      Py_DECREF(args);
+      if (!maps) return nullptr;
+    }
+    PyObject* r = PyTuple_New(2);
+    if (!r) {
+      Py_DECREF(maps);
+      return nullptr;
+    }
     PyTuple_SET_ITEM(r, 0, PyLong_FromLong(st));
-    for (int i = 0; i < 8; ++i) PyTuple_SET_ITEM(r, i + 1, wrap(o[i]));
+    PyTuple_SET_ITEM(r, 1, maps);
     return r;
   });
 }
@@ -279,6 +298,23 @@ PyObject* store_index_keys(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// One a device and stream, guarded by the GIL; never destroyed: the CUDA
+// context may be gone before static destructors run.
+std::map<std::pair<int, cudaStream_t>, at::Tensor>& kept_workspaces() {
+  static auto* kept = new std::map<std::pair<int, cudaStream_t>, at::Tensor>;
+  return *kept;
+}
+
+// () -> None: forgets the kept workspaces.
+PyObject* drop_workspaces(PyObject*, PyObject* const*, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 0);
+    kept_workspaces().clear();
+    Py_INCREF(Py_None);
+    return Py_None;
+  });
+}
+
 // The workspace kept for a stream; under graph capture a new one, which the
 // graph owns (replays must not meet eager calls in it).  Only its counters
 // need zeroing, in stream order.
@@ -294,9 +330,7 @@ at::Tensor attention_workspace(size_t bytes, const at::Tensor& like, cudaStream_
     throw std::runtime_error("the stream's capture status cannot be read");
   }
   if (cs != cudaStreamCaptureStatusNone) return fresh();
-  // never destroyed: the CUDA context may be gone before static destructors run
-  static auto* kept = new std::map<std::pair<int, cudaStream_t>, at::Tensor>;  // guarded by the GIL
-  at::Tensor& w = (*kept)[{(int)like.device().index(), stream}];
+  at::Tensor& w = kept_workspaces()[{(int)like.device().index(), stream}];
   if (!w.defined() || w.numel() < (int64_t)bytes) w = fresh();
   return w;
 }
@@ -408,6 +442,7 @@ PyMethodDef methods[] = {
     {"store_paged_kv", fast(store_paged_kv), METH_FASTCALL, nullptr},
     {"store_index_keys", fast(store_index_keys), METH_FASTCALL, nullptr},
     {"paged_attention", fast(paged_attention), METH_FASTCALL, nullptr},
+    {"drop_workspaces", fast(drop_workspaces), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

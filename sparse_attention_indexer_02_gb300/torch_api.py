@@ -23,7 +23,7 @@ class _Binding:
         except ImportError as e:
             raise RuntimeError("_qsa_torch is not built for this torch: run "
                                "`python -c 'import __graft_entry__ as g; g.build()'`") from e
-        for n in ("build_page_maps", "store_paged_kv", "store_index_keys", "paged_attention"):
+        for n in ("build_page_maps", "store_paged_kv", "store_index_keys", "paged_attention", "drop_workspaces"):
             setattr(self, n, getattr(mod, n))
         return getattr(mod, name)
 
@@ -175,11 +175,11 @@ def build_page_maps(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pag
         with _on(stream):
             return build_page_maps(context_lens, new_lens, free_pages, block_table, page_tokens=page_tokens,
                                    max_tokens=max_tokens, ratio=ratio, partial_cols=partial_cols, out=out)
-    st, *maps = _qsa_torch.build_page_maps(context_lens, new_lens, free_pages, block_table, page_tokens, max_tokens,
-                                           ratio, partial_cols, out)
+    st, maps = _qsa_torch.build_page_maps(context_lens, new_lens, free_pages, block_table, page_tokens, max_tokens,
+                                          ratio, partial_cols, out, PageMaps)
     if st:
         _abi._check(st)
-    return PageMaps._make(maps) if out is None else out
+    return maps
 
 
 def store_paged_kv(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
@@ -245,3 +245,10 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if st:
         _abi._check(st)
     return out if lse is None else (out, lse)
+
+
+def drop_attention_workspaces() -> None:
+    """Forget the workspaces paged_attention keeps: for after a call that set
+    bit 3 of device_status, which may leave their counters uncleared (the next
+    call on each stream makes a new one)."""
+    _qsa_torch.drop_workspaces()

@@ -560,8 +560,8 @@ def test_attention_odd_pages(cuda, pt):
 
 
 @gpu
-@pytest.mark.parametrize("form", [_abi.ATTN_GATHER, _abi.ATTN_TILE], ids=["gather", "tile"])
-@pytest.mark.parametrize("group", [65, 100, 128])
+@pytest.mark.parametrize("form,group", [(f, g) for f in (_abi.ATTN_GATHER, _abi.ATTN_TILE) for g in (65, 100, 128)] +
+                         [(_abi.ATTN_GATHER, 256)])
 def test_attention_wide_groups(cuda, form, group):
     pr = Problem([(300, 5), (131, 1)], 1, group, 64, 64, "bf16", seed=group)
     out, lse = pr.run(form=form)
@@ -690,6 +690,16 @@ def test_attention_one_workspace_serves_both_forms(cuda):
     ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
     for pr in (a, b, a, b, a):
         pr.check(*pr.run(workspace=ws, max_new=pr.lens[0][1]))
+
+
+@gpu
+def test_kept_workspaces_dropped(cuda):
+    pr = Problem([(9000, 1)], 2, 4, 128, 64, "bf16", seed=6)
+    want = pr.run()
+    torch.cuda.synchronize()
+    torch_api.drop_attention_workspaces()
+    got = pr.run()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 @gpu
