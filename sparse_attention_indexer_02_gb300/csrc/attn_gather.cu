@@ -12,7 +12,7 @@
 // query rows do at most 32 flop a byte (9 requests x 4 rows at 64-128K tokens:
 // 486 us, 7.1 TB/s), random 256-byte rows of HBM for selected decode (16 x 8256
 // keys: 50 us, of which copies alone are 49), the consumers' chain of steps for
-// selected chunks, whose rows come from L2 (512 rows x 2148 keys: 117 us; copies
+// selected chunks, whose rows come from L2 (512 rows x 2148 keys: 115 us; copies
 // alone 81).  So the kernel is a stream first.  Eight consumer warps work on 16
 // keys each of a 128-key unit, every one alone, with a ring of kStages 16-key
 // stages of its own; producer warps fill the rings, 32 rows at a time: a lane
@@ -444,14 +444,6 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
                   if (!seen) x[mt][n][e] = -INFINITY;
                 }
           }
-          // values: transposed loads, lanes 0-15 rows 0-15 of columns 0-7, lanes 16-31 of columns
-          // 8-15; one row tile has the registers to start them before the softmax
-          const uint32_t v_addr = kb + kSlice * L::kRow + (lane & 15) * L::kRow + (lane >> 4) * 16;
-          uint32_t bv[D / 16][4];
-          if (MT == 1) {
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) ldsm4t(bv[i], v_addr + i * 32);
-          }
           // m is raised when a maximum passes it by more than 8 only: any m that keeps the
           // exponentials in range gives the same quotient, and raising costs a pass over o.
           // So a row's lanes look at their own scores, and find the row's maximum only then.
@@ -496,13 +488,17 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
               pa[mt][h] = pack2<F16>(pr[0], pr[1]);
               pa[mt][2 + h] = pack2<F16>(pr[2], pr[3]);
             }
+          // values: transposed loads, lanes 0-15 rows 0-15 of columns 0-7, lanes 16-31 of columns
+          // 8-15 (all before the softmax, to overlap it: 2 us slower on the selected chunk)
+          const uint32_t v_addr = kb + kSlice * L::kRow + (lane & 15) * L::kRow + (lane >> 4) * 16;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            if (MT > 1) ldsm4t(bv[i], v_addr + i * 32);
+            uint32_t bv[4];
+            ldsm4t(bv, v_addr + i * 32);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-              mma16816<F16>(o[mt][2 * i], pa[mt], bv[i][0], bv[i][1]);
-              mma16816<F16>(o[mt][2 * i + 1], pa[mt], bv[i][2], bv[i][3]);
+              mma16816<F16>(o[mt][2 * i], pa[mt], bv[0], bv[1]);
+              mma16816<F16>(o[mt][2 * i + 1], pa[mt], bv[2], bv[3]);
             }
           }
         }
