@@ -32,9 +32,11 @@
  *     scales or logits and before it writes anything.  The row metadata -
  *     visible_cols, next_n_lens and block_table - may be read before that
  *     wait, so the kernel just before a compute call in its stream must not
- *     write them (copies, and kernels further back in the stream, may).  The
- *     library's own kernels never write them, and each of them waits for its
- *     own predecessor before it lets the next kernel start.
+ *     write them (copies, and kernels further back in the stream, may).  Of the
+ *     library's own kernels only qsa_build_page_maps writes them, and it lets
+ *     no kernel start before it has completed, so a compute call may follow it
+ *     directly; the others wait for their own predecessor before they let the
+ *     next kernel start.
  *   - Argument errors are detected on the host, before anything is enqueued,
  *     and returned synchronously (QSA_ERR_INVALID_ARG / QSA_ERR_UNSUPPORTED);
  *     a failed launch returns QSA_ERR_CUDA.  qsa_last_error() describes the
@@ -405,11 +407,9 @@ qsa_status qsa_page_stream(const void* base, int64_t page_stride, int32_t page_b
  *   qsa_paged_attention    attention of the new tokens over the paged cache, or
  *                          over the columns the top-k selected.
  *
- * The conventions above hold, with two differences.  These calls read nothing
+ * The conventions above hold, with one difference: these calls read nothing
  * before the kernel ahead of them in the stream has completed (metadata
- * included).  And qsa_build_page_maps writes block_table and visible_cols,
- * which scoring and selection read early: another kernel (the stores, in a
- * step) must stand between it and such a call in the stream.
+ * included).
  * ------------------------------------------------------------------------- */
 
 /* 16-bit element types of keys, values, queries and outputs. */

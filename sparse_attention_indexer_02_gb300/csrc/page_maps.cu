@@ -10,6 +10,11 @@
 // The tokens' own page lookups never meet a write of the launch: pages a
 // request had before come from the table, new ones straight from the free list.
 //
+// The launch does not let the next kernel in the stream start early: it writes
+// the block table and the visible counts, which the scorers load before they
+// wait for the kernel ahead of them.  A grid that never releases its dependents
+// has completed, its writes visible, when they start.
+//
 // Bound by latency at every size that occurs (28 bytes a token): the launch, the
 // lengths' load, the scan, a search and a page lookup one after the other; 3.8 us
 // for 16 requests of a token, 5.3 for 512 requests and 33 K tokens.
@@ -60,8 +65,7 @@ __global__ void __launch_bounds__(kNT) page_maps_kernel(const PageMapsParams p) 
   int32_t* first = sums + B + 1;  // [B + 1] new pages before request b
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  ptx::grid_dep_wait();
-  ptx::grid_dep_launch();
+  ptx::grid_dep_wait();  // (and no grid_dep_launch: see above)
 
   // each thread sums a contiguous run of requests; the runs are then scanned
   const int per = (B + kNT - 1) / kNT;

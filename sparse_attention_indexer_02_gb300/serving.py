@@ -65,8 +65,6 @@ def step(pool: PagedPool, block_table: torch.Tensor, context_lens: torch.Tensor,
         raise ValueError("rows must be a whole number of rows per request")
     maps = torch_api.build_page_maps(context_lens, new_lens, free_pages, block_table, page_tokens=pool.page_tokens,
                                      max_tokens=T, ratio=pool.ratio)
-    # the stores stand between the maps and the scoring, which reads the table
-    # and the visible counts while the kernel before it finishes
     torch_api.store_paged_kv(k, v, maps.slots, pool.k_cache, pool.v_cache)
     torch_api.store_index_keys(index_keys, maps.column_slots, pool.index, **pool.index_args)
     cols = max(1, max_context // pool.ratio)

@@ -1,0 +1,72 @@
+"""Edges of the serving operators: calls in other orders, on other streams, and
+with other layouts and lengths than a plain step's (the operators themselves:
+test_serving_ops.py)."""
+import os
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import sparse_attention_indexer_02_gb300 as qsa  # noqa: E402
+from sparse_attention_indexer_02_gb300 import build as qbuild  # noqa: E402
+from sparse_attention_indexer_02_gb300 import torch_api  # noqa: E402
+from test_serving_ops import _cu, cuda, gpu, lib  # noqa: E402,F401
+
+
+# ---------------------------------------------------------------------------
+# page maps directly before a call that reads them early
+# ---------------------------------------------------------------------------
+
+def test_page_maps_release_no_kernel_early():
+    """The scorers load visible_cols and block_table before they wait for the
+    kernel ahead of them, so the kernel that writes both must not release them."""
+    with open(os.path.join(qbuild.CSRC, "page_maps.cu")) as f:
+        code = [line.split("//")[0] for line in f]
+    assert not any("grid_dep_launch" in line or "launch_dependents" in line for line in code)
+
+
+@gpu
+@pytest.mark.parametrize("captured", [False, True])
+def test_scoring_directly_after_page_maps(cuda, captured):
+    """The maps' table and counts, not what the buffers held before."""
+    B, pt, ratio, cols = 64, 64, 4, 512
+    g = torch.Generator(device="cuda").manual_seed(1)
+    r = np.random.default_rng(1)
+    pool = torch.randn((B * 33, pt // ratio, 128), generator=g, device="cuda").to(torch.bfloat16)
+    q = torch.randn((B, 8, 128), generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.rand((B, 8), generator=g, device="cuda")
+    ctx, new, free, table = _cu([0] * B), _cu([1] * B), _cu([0] * B), _cu(np.zeros((B, 33)))
+    out = torch_api.PageMaps(_cu([0] * (B + 1)), _cu([0] * B), _cu([0] * B, torch.int64), _cu([0] * B), _cu([0] * B),
+                             _cu([0] * B), _cu([0] * B, torch.int64), _cu([0]))
+
+    def score():
+        return torch_api.paged_mqa_logits(q, w, pool, table, out.visible_cols, page_cols=pt // ratio, out_cols=cols)
+
+    def both():
+        torch_api.build_page_maps(ctx, new, free, table, page_tokens=pt, max_tokens=B, ratio=ratio, out=out)
+        return score()
+
+    both()
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            kept = both()
+    for _ in range(10):
+        c = r.integers(0, 32 * pt, B)
+        c[::3] = c[::3] // pt * pt    # these begin a page
+        pages = r.permutation(B * 33)
+        t = np.zeros((B, 33), np.int64)
+        have = -(-c // pt)
+        for b in range(B):
+            t[b, :have[b]] = pages[b * 32:b * 32 + have[b]]
+        ctx.copy_(_cu(c)), free.copy_(_cu(pages[-B:])), table.copy_(_cu(t)), out.visible_cols.zero_()
+        if captured:
+            graph.replay()
+            got = kept
+        else:
+            got = both()
+        torch.cuda.synchronize()
+        assert out.visible_cols.tolist() == ((c + 1) // ratio).tolist()
+        assert torch.equal(got, score())
