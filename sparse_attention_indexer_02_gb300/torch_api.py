@@ -143,9 +143,11 @@ def paged_mqa_topk(q: torch.Tensor, weights: torch.Tensor, kv_cache: torch.Tenso
 # not fit a call raise ValueError, a status of the C ABI other than OK QSAError.
 
 def _on(stream):
-    """Context in which a call's launches and allocations belong to `stream`."""
+    """Context in which a call's launches and allocations belong to `stream`
+    (a stream, or a handle; ExternalStream takes handle 0, the default stream's,
+    for "none given" and makes another stream)."""
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
     return torch.cuda.stream(stream)
 
 

@@ -70,3 +70,38 @@ def test_scoring_directly_after_page_maps(cuda, captured):
         torch.cuda.synchronize()
         assert out.visible_cols.tolist() == ((c + 1) // ratio).tolist()
         assert torch.equal(got, score())
+
+
+# ---------------------------------------------------------------------------
+# stream handles
+# ---------------------------------------------------------------------------
+
+def test_stream_handle_zero_is_the_default_stream(monkeypatch):
+    """ExternalStream(0) is some stream of torch's pool: never made for handle 0."""
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: ("external", handle))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda: "default")
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    assert torch_api._on(0) == "default"
+    assert torch_api._on(1234) == ("external", 1234)
+    assert torch_api._on("a stream") == "a stream"
+
+
+@gpu
+def test_calls_given_the_default_streams_handle(cuda):
+    """The handle of the default stream, from another stream's context: the call is
+    ordered with the default stream's work."""
+    handle = torch.cuda.default_stream().cuda_stream
+    with torch_api._on(handle):
+        assert torch.cuda.current_stream().cuda_stream == handle
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with torch_api._on(handle):
+            assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    k = torch.ones((64, 1, 64), dtype=torch.bfloat16, device="cuda")
+    slots, cache = torch.arange(64, device="cuda"), torch.zeros((2, 1, 64, 1, 64), dtype=torch.bfloat16, device="cuda")
+    big = torch.ones(1 << 28, device="cuda")
+    for i in range(1, 4):
+        for _ in range(4):
+            big.mul_(1.0)          # the default stream is busy when the call is made
+        k.fill_(float(i))
+        torch_api.store_paged_kv(k, k, slots, cache[0], cache[1], stream=handle)
+        assert (cache == i).all()
