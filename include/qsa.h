@@ -582,7 +582,9 @@ typedef struct qsa_attn_desc {
  * block_table int32; query_start int32 [B+1], non-decreasing, clamped to
  * [0, num_tokens]; seq_lens int32 [B]; selected int32 [num_tokens][num_selected]
  * or NULL when num_selected is 0; lse fp32 [num_tokens][num_q_heads] or NULL.
- * Page ids are clamped to [0, num_pages).
+ * A table entry of -1, as qsa_build_page_maps marks a page the free list had no
+ * more of, holds no tokens: no row sees those.  Other page ids are clamped to
+ * [0, num_pages).
  * workspace: device memory of at least qsa_paged_attention_workspace(desc)
  * bytes, 16-byte aligned, whose first QSA_ATTN_COUNTER_BYTES are zero before
  * its first use; every completed call leaves them zero again, whatever its

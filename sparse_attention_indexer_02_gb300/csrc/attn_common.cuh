@@ -28,6 +28,7 @@ namespace attn {
 constexpr int kUnit = 128;      // keys a unit
 constexpr int kMaxGrid = 160;   // CTAs a launch, at most (GB300 has 152 SMs)
 static_assert(kMaxGrid * 4 == QSA_ATTN_COUNTER_BYTES, "one counter a CTA");
+constexpr int32_t kNoPage = -1; // block-table entry: the page is missing (free list exhausted), its tokens are not seen
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr long long kSpin = 2000000000LL;  // about one second of SM clocks
 

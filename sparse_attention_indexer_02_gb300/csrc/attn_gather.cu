@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
       }
 
       for (int j = ua; j < uz && ok; j += kStep) {
-        const uint32_t vm = __ballot_sync(0xffffffffu, tok >= 0);
+        const uint32_t vm = __ballot_sync(0xffffffffu, tok >= 0 && page != kNoPage);
         const int32_t pg = min(max(page, 0), p.num_pages - 1), tk = max(tok, 0);
         const int32_t off = p.page_shift >= 0 ? tk & (p.page_tokens - 1) : tk % p.page_tokens;
         const int64_t ko = (int64_t)kvh * p.k_head_stride + (int64_t)pg * p.k_page_stride + (int64_t)off * p.k_token_stride;
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
             for (int e = 0; e < 8; ++e) x[0][e >> 2][e & 3] += y[0][e >> 2][e & 3];
           }
           const int32_t key0 = j * kUnit + warp * kSlice;
-          if (SEL ? vm != 0xFFFFu : key0 + kSlice > all_see) {
+          if (vm != 0xFFFFu || (!SEL && key0 + kSlice > all_see)) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const int c = n * 8 + (lane & 3) * 2 + (e & 1);
-                  const bool seen = SEL ? (vm >> c) & 1u : key0 + c < lim[mt][e >> 1];
+                  const bool seen = ((vm >> c) & 1u) && (SEL || key0 + c < lim[mt][e >> 1]);
                   if (!seen) x[mt][n][e] = -INFINITY;
                 }
           }

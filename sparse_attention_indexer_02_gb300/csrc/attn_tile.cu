@@ -32,7 +32,9 @@
 // the last one a tile sees are masked in S; the values there are zeroed in
 // shared memory by the MMA warp before it uses them (up to the next multiple of
 // 16 keys, the product stops there), so nothing that a page holds past a
-// request's end enters a product.
+// request's end enters a product.  A missing page is loaded from past the pool's
+// last page, which the copies fill with zeros, and its keys are masked in S,
+// from a word a key tile that the copying warp leaves.
 //
 // Schedule: equal shares of the (item, 128-key) units (attn_common.cuh).  Items
 // that lie in several CTAs leave unnormalised parts; a second, small launch
@@ -224,6 +226,11 @@ __global__ void __launch_bounds__(kNT, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ SchedShared sched_sh;
   __shared__ ItemInfo item_sh[2];  // by turns, from the copying warp
+  // Missing keys of a key tile, a bit for each 8, from the copying warp, by turns.  Tile T's is
+  // written when its key stage is free.  Of five stages that is when the product with tile
+  // T - 3's values is done, of eight when the scores of tile T - 4 are, which come after the
+  // probabilities of T - 5: the softmax warps have at most five tiles' words to read yet.
+  __shared__ volatile uint32_t missing_sh[8];
   uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::bars);
   uint64_t* empty = full + kStages;
@@ -321,14 +328,20 @@ __global__ void __launch_bounds__(kNT, 1)
         for (int j = ua; j < uz && ok; ++j) {
           const int valid = min(kUnit, it.keys - j * kUnit);
           const int nb = valid > 0 ? (valid + box - 1) / box : 0;
-          const int32_t pg = min(max(page, 0), p.num_pages - 1);
+          // past the pool's end the copies write zeros
+          const int32_t pg = page == kNoPage ? p.num_pages : min(max(page, 0), p.num_pages - 1);
+          const uint32_t missing = __reduce_or_sync(
+              0xffffffffu, page == kNoPage ? ((1u << (box >> 3)) - 1u) << (lane * (box >> 3)) : 0u);
           page = page_at(j + 1);
           const int off = (j * kUnit + lane * box) % p.page_tokens;
           for (int kv = 0; kv < 2 && ok; ++kv, ++r) {
             const int st = r % kStages;
             ok = __all_sync(0xffffffffu, wait_phase(&empty[st], ((r / kStages) & 1u) ^ 1u, abort_flag, p.fault));
             if (!ok) break;
-            if (lane == 0) ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(nb * box * 128 * G::kHalves));
+            if (lane == 0) {
+              if (kv == 0) missing_sh[(r >> 1) & 7u] = missing;  // r: two stages a tile
+              ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(nb * box * 128 * G::kHalves));
+            }
             __syncwarp();
             if (lane < nb)
               for (int h = 0; h < G::kHalves; ++h)
@@ -458,6 +471,7 @@ __global__ void __launch_bounds__(kNT, 1)
       const uint64_t sc2 = pack_f32x2(sc, sc);
       const float raise = kRaise / sc;  // in units of S
       uint32_t tiles = 0, items = 0;
+      uint32_t before = 0;  // key tiles of the CTA's items before this one
       bool ok = true;
       for (uint32_t k = 0;; ++k) {
         ok = __all_sync(0xffffffffu, wait_phase(&q_bar[0], k & 1u, abort_flag, p.fault));
@@ -475,9 +489,29 @@ __global__ void __launch_bounds__(kNT, 1)
             ok = __all_sync(0xffffffffu, wait_phase(&s_full[st], tiles & 1u, abort_flag, p.fault));
             if (!ok) break;
             ptx::tc_fence_after();
+            const uint32_t missing = missing_sh[(before + (uint32_t)(j - ua)) & 7u];
             uint32_t x[4][32];
             ptx::tmem_ld32(t_s, x[0]);
             ptx::tmem_ld32(t_s + 32, x[1]);
+            // Missing pages: masked in TMEM, out of the loop's registers.  (In x, in the block of
+            // the edge below: the loop's code grows, 8K new tokens at 32K 5 % slower; here 0 to 2 %.)
+            if (__builtin_expect(__any_sync(0xffffffffu, missing != 0), 0)) {
+              ptx::tmem_ld_wait();
+#pragma unroll 1
+              for (int q = 0; q < 4; ++q) {
+                uint32_t y[32];
+                ptx::tmem_ld32(t_s + q * 32, y);
+                ptx::tmem_ld_wait();
+                ptx::tmem_ld_done32(y);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if ((missing >> (q * 4 + i / 8)) & 1u) y[i] = 0xFF800000u;
+                ptx::tmem_st32(t_s + q * 32, y);
+              }
+              ptx::tmem_st_wait();
+              ptx::tmem_ld32(t_s, x[0]);
+              ptx::tmem_ld32(t_s + 32, x[1]);
+            }
             ptx::tmem_ld_wait();
             ptx::tmem_ld_done32(x[0]);
             ptx::tmem_ld_done32(x[1]);
@@ -618,6 +652,7 @@ __global__ void __launch_bounds__(kNT, 1)
             ptx::tc_fence_before();  // O read before the next item's products (through p_ready)
           }
         }
+        before += (uint32_t)(uz - ua);
         if (!ok || it.last) break;
       }
     }

@@ -227,9 +227,10 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     with return_lse (or a given lse tensor) also lse fp32 [T, num_q_heads].
 
     q: [T, num_q_heads, head_dim] in the caches' type, any token and head
-    strides; caches as in store_paged_kv; block_table: int32 [B, max_pages];
-    query_start: int32 [B + 1]; seq_lens: int32 [B].  scale: 1/sqrt(head_dim)
-    unless given.  max_new: the host's bound on a request's new tokens (0:
+    strides; caches as in store_paged_kv; block_table: int32 [B, max_pages]
+    (tokens of an entry of -1, a page build_page_maps could not get, are not
+    seen); query_start: int32 [B + 1]; seq_lens: int32 [B].  scale:
+    1/sqrt(head_dim) unless given.  max_new: the host's bound on a request's new tokens (0:
     unknown), which only chooses the kernel form.  selected: int32 [T, k]
     columns of `ratio` tokens (select_topk's output): a row then sees these and
     its last `local_tokens` tokens only.

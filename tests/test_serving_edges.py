@@ -10,8 +10,8 @@ torch = pytest.importorskip("torch")
 
 import sparse_attention_indexer_02_gb300 as qsa  # noqa: E402
 from sparse_attention_indexer_02_gb300 import build as qbuild  # noqa: E402
-from sparse_attention_indexer_02_gb300 import torch_api  # noqa: E402
-from test_serving_ops import _cu, cuda, gpu, lib  # noqa: E402,F401
+from sparse_attention_indexer_02_gb300 import _abi, torch_api  # noqa: E402
+from test_serving_ops import Problem, _cu, cuda, gpu, lib  # noqa: E402,F401
 
 
 # ---------------------------------------------------------------------------
@@ -105,3 +105,60 @@ def test_calls_given_the_default_streams_handle(cuda):
         k.fill_(float(i))
         torch_api.store_paged_kv(k, k, slots, cache[0], cache[1], stream=handle)
         assert (cache == i).all()
+
+
+# ---------------------------------------------------------------------------
+# pages the free list had no more of
+# ---------------------------------------------------------------------------
+
+def _short_of_pages(lens, hkv, group, D, pt, dt, lost, seed):
+    """A problem some of whose table entries are -1 (lost: of request b, pages
+    lost[b]), and the columns of one token, -1 past them, that its rows still
+    see.  Page 0, what a clamped -1 would read, holds NaN."""
+    pr = Problem(lens, hkv, group, D, pt, dt, seed=seed)
+    last = pr.kc.shape[0] - 1
+    pr.kc, pr.vc = pr.kc.flip(0), pr.vc.flip(0)     # the page of NaNs first
+    pr.table = last - pr.table
+    there, held = pr.table.clone(), []
+    for b, (s, n) in enumerate(lens):
+        gone = [j for j in lost[b] if j * pt < s]
+        pr.table[b, gone] = -1
+        mine = np.array([t for t in range(max(s, 0)) if t // pt not in gone] or [-1])
+        held += [mine] * n
+    wide = max(len(m) for m in held)
+    cols = np.full((len(held), wide), -1)
+    for i, m in enumerate(held):
+        cols[i, :len(m)] = m
+    return pr, there, _cu(cols)
+
+
+LOST = {
+    "last": ([(700, 1), (70, 3), (5, 2)], [[10], [1], []]),
+    "some": ([(700, 4), (300, 1), (64, 64)], [[0, 3, 4, 9], [2], []]),
+    "all": ([(130, 2), (64, 1)], [list(range(99)), []]),
+    "chunk": ([(900, 300), (513, 130)], [[1, 2, 7, 14], [0, 8]]),
+    "long": ([(20000, 3), (9000, 1)], [list(range(0, 400, 3)), list(range(5, 120))]),
+}
+
+
+@gpu
+@pytest.mark.parametrize("form", [_abi.ATTN_GATHER, _abi.ATTN_TILE], ids=["gather", "tile"])
+@pytest.mark.parametrize("hkv,group,D,pt,dt", [(2, 4, 128, 64, "bf16"), (1, 7, 64, 8, "fp16"), (1, 2, 128, 32, "fp16"),
+                                               (1, 16, 64, 128, "bf16"), (1, 20, 128, 256, "bf16")])
+@pytest.mark.parametrize("lost", list(LOST))
+def test_attention_does_not_see_missing_pages(cuda, form, lost, hkv, group, D, pt, dt):
+    lens, gone = LOST[lost]
+    pr, there, cols = _short_of_pages(lens, hkv, group, D, pt, dt, gone, seed=pt)
+    out, lse = pr.run(form=form)
+    pr.table = there
+    pr.check(out, lse, cols, 1, 0)
+
+
+@gpu
+@pytest.mark.parametrize("local", [0, 70])
+def test_selected_attention_does_not_see_missing_pages(cuda, local):
+    pr, there, cols = _short_of_pages([(700, 4), (300, 1)], 2, 4, 128, 64, "bf16", [[0, 3, 10], [4]], seed=2)
+    every = torch.arange(175, dtype=torch.int32, device="cuda").repeat(5, 1)
+    out, lse = pr.run(selected=every, ratio=4, local_tokens=local)
+    pr.table = there
+    pr.check(out, lse, cols, 1, 0)
