@@ -574,7 +574,7 @@ typedef struct qsa_attn_desc {
  *   out[t][h] = sum_j exp(x_j - lse) V_j,   lse[t][h] = log(sum_j exp(x_j)),
  * accumulated in fp32 (the probabilities enter the second product in the
  * 16-bit type); a row that sees nothing gets zeros and -inf.
- * Rows t >= query_start[B] are not written.  Cache contents past seq_lens[b],
+ * Rows outside [query_start[0], query_start[B]) are not written.  Cache contents past seq_lens[b],
  * and pages no listed entry names, are never used, whatever they hold (NaN
  * included); the visible tokens' keys and values are finite.
  *

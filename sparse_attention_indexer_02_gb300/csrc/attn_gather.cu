@@ -136,7 +136,8 @@ constexpr int64_t part_floats() {
   return 16 * MT * (D + 2);
 }
 
-// The item of unit u of a selected call: one token row of one virtual head.
+// The item of unit u of a selected call: one token row of one virtual head.  A
+// row before the first request's, or of none, has no tokens: nothing is written.
 __device__ __forceinline__ Item selected_item(const AttnParams& p, int64_t u, int32_t units, int32_t from_b) {
   Item it;
   const int64_t i = u / units;
@@ -145,7 +146,6 @@ __device__ __forceinline__ Item selected_item(const AttnParams& p, int64_t u, in
   it.s0 = i * units;
   it.s1 = it.s0 + units;
   it.row0 = t;
-  it.n = 1;
   it.i0 = 0;
   int lo = from_b, hi = p.num_requests;  // the last request that starts at or before t
   while (hi - lo > 1) {
@@ -155,7 +155,8 @@ __device__ __forceinline__ Item selected_item(const AttnParams& p, int64_t u, in
   }
   it.b = lo;
   const Request r = request_of(p, lo);
-  it.pos0 = t < r.first + r.n ? r.pos0 + (t - r.first) : -1;
+  it.n = t >= r.first && t < r.first + r.n ? 1 : 0;
+  it.pos0 = it.n > 0 ? r.pos0 + (t - r.first) : -1;
   it.keys = min(max(it.pos0 + 1, 0), p.capacity);
   return it;
 }

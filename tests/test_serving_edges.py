@@ -162,3 +162,49 @@ def test_selected_attention_does_not_see_missing_pages(cuda, local):
     out, lse = pr.run(selected=every, ratio=4, local_tokens=local)
     pr.table = there
     pr.check(out, lse, cols, 1, 0)
+
+
+# ---------------------------------------------------------------------------
+# some requests of a larger batch
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("selected", [False, True])
+@pytest.mark.parametrize("max_new", [1, 64])
+def test_attention_of_the_later_requests_of_a_batch(cuda, selected, max_new):
+    """Metadata of requests 2 and 3 beside all rows of q: the rows before theirs,
+    and past them, are left alone."""
+    pr = Problem([(300, 5), (64, 9), (200, 3), (131, 4), (90, 2)], 2, 4, 128, 32, "bf16", seed=31)
+    T, H, D = pr.q.shape
+    kw = {}
+    if selected:
+        cols = torch.arange(75, dtype=torch.int32, device="cuda").repeat(T, 1)
+        kw = dict(selected=cols, ratio=4, local_tokens=7)
+    want = pr.run(max_new=max_new, **kw)
+    out, lse = torch.full_like(want[0], 7.0), torch.full_like(want[1], 7.0)
+    torch_api.paged_attention(pr.q, pr.kc, pr.vc, pr.table[2:4], pr.start[2:5], pr.seq[2:4], scale=pr.scale,
+                              max_new=max_new, out=out, lse=lse, **kw)
+    first, end = int(pr.start[2]), int(pr.start[4])
+    u = torch.finfo(torch.bfloat16).eps
+    mine = out[first:end].float(), want[0][first:end].float()
+    # the same sums split over the CTAs in other places: two roundings of the output apart, and of the terms
+    assert ((mine[0] - mine[1]).abs() <= 2 * u * pr.vc.nan_to_num().abs().max().float()).all()
+    assert ((lse[first:end] - want[1][first:end]).abs() <= 1e-4).all()
+    for x in (out, lse):
+        assert (x[:first] == 7).all() and (x[end:] == 7).all()
+
+
+@gpu
+def test_selected_rows_of_no_request(cuda):
+    """Decreasing row starts: the rows of the second request are nobody's."""
+    pr = Problem([(300, 40), (64, 3)], 2, 4, 128, 32, "bf16", seed=32)
+    cols = torch.arange(75, dtype=torch.int32, device="cuda").repeat(43, 1)
+    want = pr.run(selected=cols, ratio=4)
+    pr.start = _cu([0, 40, 20])
+    out = torch.full_like(want[0], 7.0)
+    pr.run(selected=cols, ratio=4, out=out)
+    assert torch.equal(out[40:], torch.full_like(out[40:], 7.0))
+    pr.start = _cu([3, 10, 43])       # rows 0-2 are nobody's
+    out = torch.full_like(want[0], 7.0)
+    pr.run(selected=cols, ratio=4, out=out)
+    assert (out[:3] == 7).all() and not (out[3:] == 7).all(2).any()
