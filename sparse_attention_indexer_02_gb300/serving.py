@@ -59,16 +59,24 @@ def step(pool: PagedPool, block_table: torch.Tensor, context_lens: torch.Tensor,
     key of the column a token completes; other rows are ignored) and
     index_weights [T, index heads] are request-major.  max_context bounds the
     requests' tokens.  A token attends to the top_k complete columns its index
-    scores select and to its last local_tokens tokens."""
+    scores select and to its last local_tokens tokens.
+
+    Views are taken as they are; of block_table (columns of a wider table),
+    index_q and index_weights the scoring gets a contiguous copy."""
     T, B = q.shape[0], block_table.shape[0]
-    if B == 0 or T % B:
+    if B == 0 or T == 0 or T % B:
         raise ValueError("rows must be a whole number of rows per request")
+    index_q, index_weights = index_q.contiguous(), index_weights.contiguous()
+    torch_api._check_scored(index_q, index_weights, block_table)  # before anything is launched
+    if index_q.shape[0] != T:
+        raise ValueError("index_q must have a row a token")
     maps = torch_api.build_page_maps(context_lens, new_lens, free_pages, block_table, page_tokens=pool.page_tokens,
                                      max_tokens=T, ratio=pool.ratio)
+    scored_table = block_table.contiguous()
     torch_api.store_paged_kv(k, v, maps.slots, pool.k_cache, pool.v_cache)
     torch_api.store_index_keys(index_keys, maps.column_slots, pool.index, **pool.index_args)
     cols = max(1, max_context // pool.ratio)
-    logits = torch_api.paged_mqa_logits(index_q, index_weights, pool.index, block_table, maps.visible_cols,
+    logits = torch_api.paged_mqa_logits(index_q, index_weights, pool.index, scored_table, maps.visible_cols,
                                         out_cols=cols, **pool.index_args)
     selected = torch_api.select_topk(logits, maps.visible_cols, top_k, max_visible=cols)
     out, lse = torch_api.paged_attention(q, pool.k_cache, pool.v_cache, block_table, maps.query_start, maps.seq_lens,

@@ -31,9 +31,56 @@ class _Binding:
 _qsa_torch = _Binding()
 
 
-def _desc_from(q, kv_cache, block_table, page_cols, out_cols, kv_dtype, scale_offset):
-    R, H, D = q.shape
-    B, max_pages = block_table.shape
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _dense(t, dtype, n):
+    return t.dtype is dtype and t.is_contiguous() and t.numel() >= n
+
+
+def _check_scored(q, weights, block_table):
+    """The scorers take these by address and shape alone."""
+    _need(q.dim() == 3 and q.is_contiguous() and q.element_size() <= 2 and q.dtype is not torch.float16,
+          "q must be a contiguous bf16 (or e4m3) [R, H, 128] tensor")
+    _need(_dense(weights, torch.float32, q.shape[0] * q.shape[1]), "weights must be a contiguous fp32 [R, H] tensor")
+    _need(block_table.dim() == 2 and block_table.dtype is torch.int32,
+          "block_table must be an int32 [num_requests, max_pages] tensor")
+
+
+def _refuse(q, weights, kv_cache, block_table, visible_cols, next_n_lens, out, out_cols):
+    """Says what of a scoring call's tensors does not fit."""
+    _check_scored(q, weights, block_table)
+    R, B = q.shape[0], block_table.shape[0]
+    _need(block_table.is_contiguous(), "block_table must be contiguous (a slice of a wider table's columns is not)")
+    _need(_dense(visible_cols, torch.int32, R), "visible_cols must be a contiguous int32 [R] tensor")
+    _need(next_n_lens is None or _dense(next_n_lens, torch.int32, B),
+          "next_n_lens must be a contiguous int32 [num_requests] tensor")
+    _need(out is None or _dense(out, torch.float32, R * out_cols), "out must be a contiguous fp32 [R, out_cols] tensor")
+    inner = 1
+    for n, step in zip(reversed(kv_cache.shape[1:]), reversed(kv_cache.stride()[1:])):
+        _need(n == 1 or step == inner, "a page of kv_cache must be contiguous")
+        inner *= n
+
+
+def _desc_from(q, weights, kv_cache, block_table, visible_cols, next_n_lens, out, page_cols, out_cols, kv_dtype,
+               scale_offset):
+    try:
+        R, H, D = q.shape
+        B, max_pages = block_table.shape
+    except ValueError:
+        R = H = D = B = max_pages = 0
+    # the usual call in one expression (through the helpers alone: a microsecond more a call)
+    if not (q.is_contiguous() and weights.is_contiguous() and block_table.is_contiguous() and
+            visible_cols.is_contiguous() and kv_cache.is_contiguous() and next_n_lens is None and
+            q.dtype is _BF16 and weights.dtype is _F32 and block_table.dtype is _I32 and visible_cols.dtype is _I32 and
+            weights.numel() == R * H > 0 and visible_cols.numel() == R and
+            (out is None or out.dtype is _F32 and out.is_contiguous() and out.numel() == R * out_cols)):
+        _refuse(q, weights, kv_cache, block_table, visible_cols, next_n_lens, out, out_cols)
     if B == 0 or R % B:
         raise ValueError("rows must be a whole number of rows per request")
     page_stride = kv_cache.stride(0) * kv_cache.element_size()
@@ -64,8 +111,10 @@ def paged_mqa_logits(q: torch.Tensor, weights: torch.Tensor, kv_cache: torch.Ten
     block-flat layout pass kv_dtype=KV_FP8_E4M3 and the byte offset of the
     scales inside a block (page_cols * 128).  next_n_lens (int32
     [num_requests]) selects qsa_paged_mqa_logits_ragged: a request's rows past
-    its count are -inf."""
-    desc, scales, q_dtype = _desc_from(q, kv_cache, block_table, page_cols, out_cols, kv_dtype, scale_offset)
+    its count are -inf.  All but kv_cache's pages are contiguous (ValueError
+    otherwise)."""
+    desc, scales, q_dtype = _desc_from(q, weights, kv_cache, block_table, visible_cols, next_n_lens, out, page_cols,
+                                       out_cols, kv_dtype, scale_offset)
     if out is None:
         out = torch.empty((q.shape[0], out_cols), dtype=torch.float32, device=q.device)
     _abi.paged_mqa_logits(desc, q, weights, kv_cache, scales, block_table, visible_cols, out, stream,
@@ -123,7 +172,8 @@ def paged_mqa_topk(q: torch.Tensor, weights: torch.Tensor, kv_cache: torch.Tenso
     """(logits fp32 [R, out_cols], top-k int32 [R, k]) in one call
     (include/qsa.h, qsa_paged_mqa_topk); arguments as paged_mqa_logits, plus k
     and the host bound max_visible of the visible counts (0: unknown)."""
-    desc, scales, q_dtype = _desc_from(q, kv_cache, block_table, page_cols, out_cols, kv_dtype, scale_offset)
+    desc, scales, q_dtype = _desc_from(q, weights, kv_cache, block_table, visible_cols, next_n_lens, out_logits,
+                                       page_cols, out_cols, kv_dtype, scale_offset)
     R = q.shape[0]
     if out_logits is None:
         out_logits = torch.empty((R, out_cols), dtype=torch.float32, device=q.device)

@@ -10,7 +10,7 @@ torch = pytest.importorskip("torch")
 
 import sparse_attention_indexer_02_gb300 as qsa  # noqa: E402
 from sparse_attention_indexer_02_gb300 import build as qbuild  # noqa: E402
-from sparse_attention_indexer_02_gb300 import _abi, torch_api  # noqa: E402
+from sparse_attention_indexer_02_gb300 import _abi, serving, torch_api  # noqa: E402
 from test_serving_ops import Problem, _cu, cuda, gpu, lib  # noqa: E402,F401
 
 
@@ -208,3 +208,96 @@ def test_selected_rows_of_no_request(cuda):
     out = torch.full_like(want[0], 7.0)
     pr.run(selected=cols, ratio=4, out=out)
     assert (out[:3] == 7).all() and not (out[3:] == 7).all(2).any()
+
+
+# ---------------------------------------------------------------------------
+# layouts of what the scoring takes
+# ---------------------------------------------------------------------------
+
+def test_scoring_refuses_layouts_it_would_misread(lib):
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    b16 = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    ok = dict(q=b16(4, 8, 128), weights=torch.zeros(4, 8), kv_cache=b16(6, 16, 128), block_table=i32(2, 3),
+              visible_cols=i32(4))
+    bad = [("block_table", i32(2, 5)[:, :3]), ("block_table", i32(2, 3).long()), ("q", b16(4, 16, 128)[:, :8]),
+           ("q", b16(4, 8, 128).half()), ("q", torch.zeros(4, 8, 128)), ("weights", b16(4, 8)),
+           ("weights", torch.zeros(4, 16)[:, :8]), ("weights", torch.zeros(4, 4)), ("visible_cols", i32(4).long()),
+           ("visible_cols", i32(8)[::2]), ("visible_cols", i32(2)), ("next_n_lens", i32(1)),
+           ("next_n_lens", i32(2).long()), ("kv_cache", b16(6, 128, 16).transpose(1, 2))]
+    for name, t in bad:
+        with pytest.raises(ValueError, match="must be"):
+            torch_api.paged_mqa_logits(**{**ok, name: t}, page_cols=16, out_cols=32, stream=0)
+        with pytest.raises(ValueError, match="must be"):
+            torch_api.paged_mqa_topk(**{**ok, name: t}, k=4, page_cols=16, out_cols=32, stream=0)
+    for out in (torch.zeros(4, 64)[:, :32], b16(4, 32), torch.zeros(4, 31)):
+        with pytest.raises(ValueError, match="out must be"):
+            torch_api.paged_mqa_logits(**ok, page_cols=16, out_cols=32, out=out, stream=0)
+
+
+def test_step_refuses_before_anything_is_launched(lib, monkeypatch):
+    def launched(*a, **k):
+        raise AssertionError("launched")
+
+    monkeypatch.setattr(torch_api, "build_page_maps", launched)
+    pool = serving.PagedPool(num_pages=4, page_tokens=64, num_kv_heads=1, head_dim=64, device="cpu")
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    b16 = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    ok = dict(block_table=i32(2, 3), context_lens=i32(2), new_lens=i32(2), free_pages=i32(2), q=b16(4, 2, 64),
+              k=b16(4, 1, 64), v=b16(4, 1, 64), index_q=b16(4, 8, 128), index_keys=b16(4, 128),
+              index_weights=torch.zeros(4, 8), top_k=4, max_context=64)
+    with pytest.raises(AssertionError, match="launched"):
+        serving.step(pool, **ok)
+    for name, t in (("q", b16(3, 2, 64)), ("q", b16(0, 2, 64)), ("block_table", i32(2, 3).long()),
+                    ("index_q", b16(4, 8, 128).half()), ("index_q", b16(2, 8, 128)), ("index_weights", b16(4, 8)),
+                    ("index_weights", torch.zeros(4, 4))):
+        with pytest.raises(ValueError):
+            serving.step(pool, **{**ok, name: t})
+
+
+def _step_inputs(B, n, hkv, H, D, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    T = B * n
+    return dict(q=rnd(T, H, D), k=rnd(T, hkv, D), v=rnd(T, hkv, D), index_q=rnd(T, 4, 128), index_keys=rnd(T, 128),
+                index_weights=torch.rand((T, 4), generator=g, device="cuda"))
+
+
+def _two_steps(pool, table, B, make):
+    """A prompt of 200 tokens a request and two decode steps; the results of each."""
+    perm = torch.randperm(pool.k_cache.shape[0], generator=torch.Generator().manual_seed(3)).to(torch.int32).cuda()
+    res, ctx, taken = [], 0, 0
+    for i, n in enumerate((200, 1, 2)):
+        r = serving.step(pool, table, _cu([ctx] * B), _cu([n] * B), perm[taken:], top_k=16, local_tokens=4,
+                         max_context=256, **make(i, n))
+        res.append((r.out, r.lse, r.selected))
+        taken += int(r.maps.pages_used)
+        ctx += n
+    return res
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_step_takes_views(cuda, fp8):
+    """Columns of a wider table, index queries and weights out of a fused
+    projection: the results of contiguous ones."""
+    B, hkv, H, D = 3, 2, 8, 64
+
+    def plain(i, n):
+        return _step_inputs(B, n, hkv, H, D, i)
+
+    def views(i, n):
+        d = plain(i, n)
+        wide = torch.full((B * n, 9, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+        wide[:, 2:6] = d["index_q"]
+        w = torch.full((B * n, 7), 5.0, device="cuda")
+        w[:, 1:5] = d["index_weights"]
+        return {**d, "index_q": wide[:, 2:6], "index_weights": w[:, 1:5]}
+
+    new_pool = lambda: serving.PagedPool(num_pages=30, page_tokens=64, num_kv_heads=hkv, head_dim=D, index_fp8=fp8)  # noqa: E731
+    want = _two_steps(new_pool(), torch.full((B, 5), -1, dtype=torch.int32, device="cuda"), B, plain)
+    wide = torch.full((B, 11), -1, dtype=torch.int32, device="cuda")
+    got = _two_steps(new_pool(), wide[:, 3:8], B, views)
+    for a, b in zip(want, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+    assert (wide[:, :3] == -1).all() and (wide[:, 8:] == -1).all()
