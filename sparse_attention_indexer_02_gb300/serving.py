@@ -23,7 +23,8 @@ class PagedPool:
 
     A page holds page_tokens tokens, and page_tokens / ratio compressed index
     columns of them.  index_fp8 keeps the index keys as e4m3 with a scale each
-    (132 bytes a column in place of 256)."""
+    (132 bytes a column in place of 256, a page rounded up to 16 bytes, as the
+    scoring takes them)."""
 
     def __init__(self, num_pages: int, page_tokens: int, num_kv_heads: int, head_dim: int, ratio: int = 4,
                  dtype: torch.dtype = torch.bfloat16, index_fp8: bool = False, device="cuda"):
@@ -33,7 +34,7 @@ class PagedPool:
         kv = torch.zeros((2, num_pages, page_tokens, num_kv_heads, head_dim), dtype=dtype, device=device)
         self.k_cache, self.v_cache = kv[0], kv[1]
         if index_fp8:
-            self.index = torch.zeros((num_pages, self.page_cols * 132), dtype=torch.uint8, device=device)
+            self.index = torch.zeros((num_pages, -(-self.page_cols * 132 // 16) * 16), dtype=torch.uint8, device=device)
             self.index_args = dict(page_cols=self.page_cols, kv_dtype=_abi.KV_FP8_E4M3, scale_offset=self.page_cols * 128)
         else:
             self.index = torch.zeros((num_pages, self.page_cols, 128), dtype=torch.bfloat16, device=device)

@@ -262,12 +262,12 @@ def _step_inputs(B, n, hkv, H, D, seed):
                 index_weights=torch.rand((T, 4), generator=g, device="cuda"))
 
 
-def _two_steps(pool, table, B, make):
+def _two_steps(pool, table, B, make, top_k=16):
     """A prompt of 200 tokens a request and two decode steps; the results of each."""
     perm = torch.randperm(pool.k_cache.shape[0], generator=torch.Generator().manual_seed(3)).to(torch.int32).cuda()
     res, ctx, taken = [], 0, 0
     for i, n in enumerate((200, 1, 2)):
-        r = serving.step(pool, table, _cu([ctx] * B), _cu([n] * B), perm[taken:], top_k=16, local_tokens=4,
+        r = serving.step(pool, table, _cu([ctx] * B), _cu([n] * B), perm[taken:], top_k=top_k, local_tokens=4,
                          max_context=256, **make(i, n))
         res.append((r.out, r.lse, r.selected))
         taken += int(r.maps.pages_used)
@@ -301,3 +301,30 @@ def test_step_takes_views(cuda, fp8):
         for x, y in zip(a, b):
             assert torch.equal(x, y)
     assert (wide[:, :3] == -1).all() and (wide[:, 8:] == -1).all()
+
+
+@pytest.mark.parametrize("pt,ratio", [(4, 4), (8, 4), (12, 4), (20, 4), (64, 4), (6, 2), (7, 1)])
+def test_pool_of_any_page_size_suits_the_scoring(lib, pt, ratio):
+    pool = serving.PagedPool(num_pages=3, page_tokens=pt, num_kv_heads=1, head_dim=64, ratio=ratio, index_fp8=True,
+                             device="cpu")
+    assert pool.index.stride(0) % 16 == 0 and pool.index.shape[1] >= 132 * pt // ratio
+    desc = _abi.make_desc(1, 1, 4, pool.page_cols, 2, 3, 8, pool.index.stride(0), kv_dtype=qsa.KV_FP8_E4M3,
+                          scale_page_stride=pool.index.stride(0))
+    qsa.plan_variant(desc)      # raises for a page stride the scorers refuse
+
+
+@gpu
+@pytest.mark.parametrize("pt", [8, 20])
+def test_step_over_odd_fp8_pages(cuda, pt):
+    """Every complete column selected: the results of 64-token pages, to the roundings
+    of sums in another order."""
+    B, hkv, H, D = 2, 2, 8, 64
+    make = lambda i, n: _step_inputs(B, n, hkv, H, D, i)  # noqa: E731
+    got, want = (_two_steps(serving.PagedPool(num_pages=60, page_tokens=p, num_kv_heads=hkv, head_dim=D, index_fp8=True),
+                            torch.full((B, 30), -1, dtype=torch.int32, device="cuda"), B, make, top_k=64)
+                 for p in (pt, 64))
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(a[2], b[2])
+        # the output's rounding on both sides and the terms' (values up to 5), bf16
+        assert ((a[0].float() - b[0].float()).abs() <= 4 * 2.0 ** -8 * 5).all(), i
+        assert ((a[1] - b[1]).abs() <= 1e-4).all(), i
