@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from typing import Optional
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -33,6 +34,7 @@ EXPORTED = ("qsa_paged_mqa_logits", "qsa_paged_mqa_logits_ragged", "qsa_paged_mq
 HALF_BF16, HALF_F16 = 0, 1
 ATTN_AUTO, ATTN_GATHER, ATTN_TILE = 0, 1, 2
 ATTN_COUNTER_BYTES = 640
+FAULT_ATTENTION = 8  # device_status: an attention launch gave up on a wait
 
 
 class QSAError(RuntimeError):
@@ -285,9 +287,15 @@ def noalloc_counters() -> tuple[int, int]:
 
 
 def device_status(clear: bool = True) -> int:
-    """Device fault word (non-zero: a kernel gave up on a barrier wait); synchronises."""
+    """Device fault word (non-zero: a kernel gave up on a barrier wait); synchronises.
+    With clear, bit 3 also makes paged_attention forget the workspaces it keeps:
+    the call that gave up may have left their counters in the middle of a count."""
     v = ctypes.c_uint32(0)
     _check(load_library().qsa_device_status(ctypes.byref(v), 1 if clear else 0))
+    if clear and v.value & FAULT_ATTENTION:
+        binding = sys.modules.get(__package__ + "._qsa_torch")  # not loaded: nothing kept
+        if binding is not None:
+            binding.drop_workspaces()
     return v.value
 
 

@@ -301,7 +301,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
 
 
 def drop_attention_workspaces() -> None:
-    """Forget the workspaces paged_attention keeps: for after a call that set
-    bit 3 of device_status, which may leave their counters uncleared (the next
-    call on each stream makes a new one)."""
+    """Forget the workspaces paged_attention keeps (the next call on each stream
+    makes a new one).  device_status does so itself when it clears bit 3, a call
+    that gave up on a wait: that may leave their counters uncleared."""
     _qsa_torch.drop_workspaces()

@@ -2,6 +2,8 @@
 with other layouts and lengths than a plain step's (the operators themselves:
 test_serving_ops.py)."""
 import os
+import sys
+import types
 
 import numpy as np
 import pytest
@@ -328,3 +330,50 @@ def test_step_over_odd_fp8_pages(cuda, pt):
         # the output's rounding on both sides and the terms' (values up to 5), bf16
         assert ((a[0].float() - b[0].float()).abs() <= 4 * 2.0 ** -8 * 5).all(), i
         assert ((a[1] - b[1]).abs() <= 1e-4).all(), i
+
+
+# ---------------------------------------------------------------------------
+# kept workspaces
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("flags,clear,dropped", [(8, True, 1), (9, True, 1), (8, False, 0), (0, True, 0), (7, True, 0)])
+def test_a_cleared_attention_fault_drops_the_kept_workspaces(monkeypatch, flags, clear, dropped):
+    """The fault is the fake's: no kernel has to give up for it."""
+    calls = []
+
+    class Library:
+        @staticmethod
+        def qsa_device_status(word, clear_it):
+            word._obj.value = flags
+            return 0
+
+    monkeypatch.setattr(_abi, "load_library", Library)
+    monkeypatch.setitem(sys.modules, qsa.__name__ + "._qsa_torch",
+                        types.SimpleNamespace(drop_workspaces=lambda: calls.append(1)))
+    assert qsa.device_status(clear=clear) == flags
+    assert len(calls) == dropped
+    monkeypatch.delitem(sys.modules, qsa.__name__ + "._qsa_torch")
+    assert qsa.device_status(clear=clear) == flags
+
+
+@gpu
+def test_the_kept_workspace_goes_with_a_reported_fault(cuda, monkeypatch):
+    """The status word as an attention launch that gave up would set it (by a fake of
+    the status call): the workspace kept for the stream is given up, the next call
+    makes a new one."""
+    pr = Problem([(9000, 1)], 2, 4, 128, 64, "bf16", seed=6)
+    want = pr.run()
+    real = _abi.load_library().qsa_device_status
+
+    def status(word, clear_it):
+        st = real(word, clear_it)
+        word._obj.value |= 8
+        return st
+
+    before = torch.cuda.memory_allocated()
+    monkeypatch.setattr(_abi, "load_library", lambda: types.SimpleNamespace(qsa_device_status=status))
+    assert qsa.device_status() & 8
+    monkeypatch.undo()
+    assert torch.cuda.memory_allocated() < before       # forgotten
+    got = pr.run()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
