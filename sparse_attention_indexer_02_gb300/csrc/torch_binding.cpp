@@ -299,9 +299,17 @@ PyObject* store_index_keys(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // One a device and stream, guarded by the GIL; never destroyed: the CUDA
-// context may be gone before static destructors run.
-std::map<std::pair<int, cudaStream_t>, at::Tensor>& kept_workspaces() {
-  static auto* kept = new std::map<std::pair<int, cudaStream_t>, at::Tensor>;
+// context may be gone before static destructors run.  At most kMaxKept, as many
+// as torch's pool has streams of a priority (5 or 43 MB each): then the one
+// unused longest goes.  Its memory returns to its own stream, so a call that
+// still runs there is not disturbed.
+struct Kept {
+  at::Tensor ws;
+  uint64_t used = 0;
+};
+constexpr size_t kMaxKept = 32;
+std::map<std::pair<int, cudaStream_t>, Kept>& kept_workspaces() {
+  static auto* kept = new std::map<std::pair<int, cudaStream_t>, Kept>;
   return *kept;
 }
 
@@ -330,9 +338,23 @@ at::Tensor attention_workspace(size_t bytes, const at::Tensor& like, cudaStream_
     throw std::runtime_error("the stream's capture status cannot be read");
   }
   if (cs != cudaStreamCaptureStatusNone) return fresh();
-  at::Tensor& w = kept_workspaces()[{(int)like.device().index(), stream}];
-  if (!w.defined() || w.numel() < (int64_t)bytes) w = fresh();
-  return w;
+  auto& kept = kept_workspaces();
+  static uint64_t calls = 0;
+  const std::pair<int, cudaStream_t> key((int)like.device().index(), stream);
+  auto at = kept.find(key);
+  if (at == kept.end() || at->second.ws.numel() < (int64_t)bytes) {
+    Kept made;
+    made.ws = fresh();
+    if (at == kept.end() && kept.size() >= kMaxKept) {
+      auto oldest = kept.begin();
+      for (auto i = kept.begin(); i != kept.end(); ++i)
+        if (i->second.used < oldest->second.used) oldest = i;
+      kept.erase(oldest);
+    }
+    at = kept.insert_or_assign(key, std::move(made)).first;
+  }
+  at->second.used = ++calls;
+  return at->second.ws;
 }
 
 // (q, k_cache, v_cache, block_table, query_start, seq_lens, scale or None, max_new, selected or None, ratio,

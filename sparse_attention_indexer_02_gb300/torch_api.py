@@ -285,7 +285,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     columns of `ratio` tokens (select_topk's output): a row then sees these and
     its last `local_tokens` tokens only.
 
-    Without a workspace, one is kept for each stream that calls; a call under
+    Without a workspace, one is kept for each stream that calls (the 32 streams
+    that called last); a call under
     graph capture gets its own, cleared again by every replay (a given
     workspace, zeroed once, spares that)."""
     if stream is not None:

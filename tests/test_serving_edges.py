@@ -377,3 +377,28 @@ def test_the_kept_workspace_goes_with_a_reported_fault(cuda, monkeypatch):
     assert torch.cuda.memory_allocated() < before       # forgotten
     got = pr.run()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@gpu
+def test_kept_workspaces_are_bounded(cuda):
+    """Calls on 64 streams (torch's pools of both priorities): at most 32 workspaces
+    stay, and a stream whose own went still gets right results."""
+    pr = Problem([(3000, 1)], 2, 4, 128, 64, "bf16", seed=14)
+    out, lse = pr.run()
+    torch.cuda.synchronize()
+    torch_api.drop_attention_workspaces()
+    streams = [torch.cuda.Stream(priority=p) for _ in range(32) for p in (0, -1)]
+    assert len({s.cuda_stream for s in streams}) > 40
+    o, z = torch.empty_like(out), torch.empty_like(lse)
+    before = torch.cuda.memory_allocated()
+    for turn in range(2):
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+            pr.run(stream=s, out=o, lse=z)
+            torch.cuda.current_stream().wait_stream(s)
+            assert torch.equal(o, out) and torch.equal(z, lse)
+    desc = _abi.AttnDesc(_abi.KvDesc(_abi.HALF_BF16, 4, 64, 2, 128, 0, 32768, 512, 256, 32768, 512, 256), 1, 8, 4, 1, 0,
+                         1, 0, _abi.ATTN_GATHER, 1, 4, 2048, 256, 2048, 256, 0.1, 0)
+    assert torch.cuda.memory_allocated() - before <= 32 * (qsa.paged_attention_workspace_bytes(desc) + 512)
+    torch_api.drop_attention_workspaces()
+    assert torch.cuda.memory_allocated() <= before
