@@ -87,11 +87,18 @@ void table(const at::Tensor& t) {
        "block_table must be an int32 [num_requests, max_pages] tensor with contiguous rows");
 }
 
-// All tensors of a call lie on one CUDA device.
+// All tensors of a call lie on one CUDA device, the current one: the library
+// launches there, whatever device the stream and the addresses are of.
 struct Place {
   c10::Device dev;
   explicit Place(const at::Tensor& t) : dev(t.device()) {
     need(dev.is_cuda(), "the tensors must be on a CUDA device");
+    int current = -1;
+    if (cudaGetDevice(&current) != cudaSuccess) {
+      cudaGetLastError();
+      current = -1;
+    }
+    need((int)dev.index() == current, "the tensors must be on the current CUDA device");
   }
   void also(const at::Tensor& t) const { need(t.device() == dev, "the tensors are on different devices"); }
   cudaStream_t stream() const { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }

@@ -402,3 +402,27 @@ def test_kept_workspaces_are_bounded(cuda):
     assert torch.cuda.memory_allocated() - before <= 32 * (qsa.paged_attention_workspace_bytes(desc) + 512)
     torch_api.drop_attention_workspaces()
     assert torch.cuda.memory_allocated() <= before
+
+
+# ---------------------------------------------------------------------------
+# tensors of another device
+# ---------------------------------------------------------------------------
+
+def test_tensors_of_another_device_are_refused(lib):
+    """Tensors that say they are on device 1 (fake ones, without memory) while
+    another device, or none, is the current one."""
+    fake = pytest.importorskip("torch._subclasses.fake_tensor")
+    with fake.FakeTensorMode():
+        z = lambda dtype, *s: torch.empty(s, dtype=dtype, device="cuda:1")  # noqa: E731
+        b16, i32, i64 = torch.bfloat16, torch.int32, torch.int64
+        kv, kc, slots, q = z(b16, 3, 2, 128), z(b16, 4, 16, 2, 128), z(i64, 3), z(b16, 3, 8, 128)
+        keys, index = z(b16, 3, 128), z(b16, 4, 16, 128)
+        two, three, four, table = z(i32, 2), z(i32, 3), z(i32, 4), z(i32, 2, 4)
+    if torch.cuda.is_available():
+        assert torch.cuda.current_device() != 1
+    for call in (lambda: torch_api.store_paged_kv(kv, kv, slots, kc, kc),
+                 lambda: torch_api.store_index_keys(keys, slots, index, page_cols=16),
+                 lambda: torch_api.build_page_maps(two, two, four, table, page_tokens=16, max_tokens=4),
+                 lambda: torch_api.paged_attention(q, kc, kc, table, three, two)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
