@@ -452,7 +452,7 @@ typedef struct qsa_page_maps_desc {
  *                       (p % ratio == ratio - 1) and has a slot, else -1.
  * Rows t in [query_start[B], max_tokens) are padding: -1, -1, -1, 0, -1.
  * Tokens past max_tokens are not written; query_start still counts them.
- * The sums saturate at 2^31-1.
+ * The sums, positions and visible counts saturate at 2^31-1.
  *
  * Device pointers: context_lens, new_lens int32 [B]; free_pages int32
  * [num_free]; block_table int32, updated in place; query_start int32 [B+1],

@@ -129,8 +129,9 @@ __global__ void __launch_bounds__(kNT) page_maps_kernel(const PageMapsParams p) 
         if (i < p.num_free) page = p.free_pages[i];
       }
       if (page >= 0) slot = (int64_t)page * p.page_tokens + off;
-      const int32_t q = (int32_t)(ps / p.ratio), r = (int32_t)(ps - (int64_t)q * p.ratio);
-      vis = q + ((p.partial_cols || r == p.ratio - 1) ? 1 : 0);
+      const int64_t q = ps / p.ratio;
+      const int32_t r = (int32_t)(ps - q * p.ratio);
+      vis = sat31(q + ((p.partial_cols || r == p.ratio - 1) ? 1 : 0));
       if (slot >= 0 && r == p.ratio - 1) col = slot / p.ratio;
     }
     p.slots[t] = slot;

@@ -426,3 +426,22 @@ def test_tensors_of_another_device_are_refused(lib):
                  lambda: torch_api.paged_attention(q, kc, kc, table, three, two)):
         with pytest.raises(ValueError, match="current CUDA device"):
             call()
+
+
+# ---------------------------------------------------------------------------
+# page maps at the end of the range
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("partial", [False, True])
+@pytest.mark.parametrize("ratio", [1, 2])
+def test_visible_counts_saturate(cuda, ratio, partial):
+    """Positions next to and past 2^31 - 1: a count of columns never turns negative."""
+    big = 2**31 - 1
+    got = torch_api.build_page_maps(_cu([big - 1]), _cu([4]), _cu([0]), _cu([[0]]), page_tokens=2, max_tokens=5,
+                                    ratio=ratio, partial_cols=partial)
+    pos = [big - 1 + i for i in range(4)]
+    vis = [min(big, -(-(p + 1) // ratio) if partial else (p + 1) // ratio) for p in pos]
+    assert got.visible_cols.tolist() == vis + [0]
+    assert got.positions.tolist() == [min(big, p) for p in pos] + [-1]
+    assert got.slots.tolist() == [-1] * 5 and got.column_slots.tolist() == [-1] * 5
