@@ -61,6 +61,15 @@ int32_t integer32(PyObject* o, const char* name) {
   return (int32_t)v;
 }
 
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    throw Refused(std::string(name) + " must be true or false");
+  }
+  return v == 1;
+}
+
 int32_t size32(int64_t v, const char* name) {
   if (v > INT32_MAX) throw Refused(std::string(name) + " does not fit 32 bits");
   return (int32_t)v;
@@ -178,7 +187,7 @@ PyObject* build_page_maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
     d.page_tokens = integer32(a[4], "page_tokens");
     d.max_pages = size32(bt.size(1), "max_pages");
     d.ratio = integer32(a[6], "ratio");
-    d.partial_cols = PyObject_IsTrue(a[7]) == 1 ? 1 : 0;
+    d.partial_cols = truth(a[7], "partial_cols") ? 1 : 0;
     d.table_stride = step_of(bt, 0);
     d.num_free = fp.size(0);
     d.max_tokens = integer(a[5], "max_tokens");
@@ -426,7 +435,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                lse.size(1) == H,
            "lse must be a contiguous fp32 [T, num_q_heads] tensor");
       place.also(lse);
-    } else if (PyObject_IsTrue(a[14]) == 1) {
+    } else if (truth(a[14], "return_lse")) {
       lse = at::empty({T, H}, q.options().dtype(at::kFloat));
     }
     d.out_token_stride = 2 * step_of(out, 0);

@@ -445,3 +445,23 @@ def test_visible_counts_saturate(cuda, ratio, partial):
     assert got.visible_cols.tolist() == vis + [0]
     assert got.positions.tolist() == [min(big, p) for p in pos] + [-1]
     assert got.slots.tolist() == [-1] * 5 and got.column_slots.tolist() == [-1] * 5
+
+
+# ---------------------------------------------------------------------------
+# arguments without a truth value
+# ---------------------------------------------------------------------------
+
+def test_flags_without_a_truth_value_are_refused(lib):
+    """An error Python raises while a flag is read is the call's own refusal, not a
+    result returned with an error pending."""
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    with pytest.raises(ValueError, match="partial_cols"):
+        torch_api.build_page_maps(i32(2), i32(2), i32(4), i32(2, 4), page_tokens=16, max_tokens=4,
+                                  partial_cols=np.zeros(2))
+
+
+@gpu
+def test_return_lse_without_a_truth_value_is_refused(cuda):
+    pr = Problem([(30, 1)], 1, 2, 64, 16, "bf16", seed=1)
+    with pytest.raises(ValueError, match="return_lse"):
+        torch_api.paged_attention(pr.q, pr.kc, pr.vc, pr.table, pr.start, pr.seq, return_lse=np.zeros(2))
