@@ -47,6 +47,16 @@ class StepResult(NamedTuple):
     selected: torch.Tensor     # int32 [T, top_k]
     maps: torch_api.PageMaps
 
+    def valid(self) -> torch.Tensor:
+        """A bool on the device, for a caller whose lengths or free pages live there
+        alone: every request brought the same number of new tokens, and every
+        token got a cache slot.  Where it is false, rows were scored for another
+        request than their own, or tokens (theirs or later ones') are not in the
+        caches and not seen; the step's results are not to be used."""
+        T, B = self.out.shape[0], self.maps.seq_lens.shape[0]
+        rows = torch.arange(B + 1, device=self.out.device) * (T // B)
+        return (self.maps.query_start == rows).all() & (self.maps.slots >= 0).all()
+
 
 def step(pool: PagedPool, block_table: torch.Tensor, context_lens: torch.Tensor, new_lens: torch.Tensor,
          free_pages: torch.Tensor, *, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, index_q: torch.Tensor,
@@ -61,6 +71,9 @@ def step(pool: PagedPool, block_table: torch.Tensor, context_lens: torch.Tensor,
     index_weights [T, index heads] are request-major.  max_context bounds the
     requests' tokens.  A token attends to the top_k complete columns its index
     scores select and to its last local_tokens tokens.
+
+    Nothing of the device is read, so neither a new_lens that holds other counts
+    nor a free list with too few pages raises: StepResult.valid() tells.
 
     Views are taken as they are; of block_table (columns of a wider table),
     index_q and index_weights the scoring gets a contiguous copy."""

@@ -465,3 +465,44 @@ def test_return_lse_without_a_truth_value_is_refused(cuda):
     pr = Problem([(30, 1)], 1, 2, 64, 16, "bf16", seed=1)
     with pytest.raises(ValueError, match="return_lse"):
         torch_api.paged_attention(pr.q, pr.kc, pr.vc, pr.table, pr.start, pr.seq, return_lse=np.zeros(2))
+
+
+# ---------------------------------------------------------------------------
+# steps whose lengths or pages do not suffice
+# ---------------------------------------------------------------------------
+
+def _one_step(new, pages, **kw):
+    """A step of 2 requests with 70 tokens each of context and 60 rows in all, over
+    64-token pages; page 0 is another request's and holds NaN."""
+    pool = serving.PagedPool(num_pages=8, page_tokens=64, num_kv_heads=1, head_dim=64)
+    pool.k_cache[0], pool.v_cache[0] = float("nan"), float("nan")
+    table = _cu([[1, 2, -1, -1], [3, 4, -1, -1]])
+    return serving.step(pool, table, _cu([70, 70]), _cu(new), _cu(pages), top_k=16, local_tokens=8, max_context=256,
+                        **_step_inputs(2, 30, 1, 4, 64, 5), **kw), table
+
+
+@gpu
+def test_step_says_whether_lengths_and_pages_sufficed(cuda):
+    good, table = _one_step([30, 30], [])
+    assert good.valid().item() is True and table.tolist() == [[1, 2, -1, -1], [3, 4, -1, -1]]
+    assert not _one_step([20, 40], [5, 6])[0].valid()          # as many rows, shared out otherwise
+    assert not _one_step([30, 29], [])[0].valid()
+    fine, _ = _one_step([30, 30], [7])
+    assert fine.valid() and torch.equal(fine.out, good.out)
+
+
+@gpu
+def test_step_without_enough_pages_reads_no_other_requests(cuda):
+    """Requests at a page's end, no page free: their new tokens are nowhere, and the
+    rows see the tokens there are, not page 0's."""
+    pool = serving.PagedPool(num_pages=8, page_tokens=64, num_kv_heads=1, head_dim=64)
+    pool.k_cache.normal_(), pool.v_cache.normal_()
+    pool.k_cache[0], pool.v_cache[0] = float("nan"), float("nan")
+    pool.index.normal_()
+    table = _cu([[1, 2, -1], [3, 4, -1]])
+    res = serving.step(pool, table, _cu([128, 128]), _cu([30, 30]), _cu([5]), top_k=16, local_tokens=8, max_context=192,
+                       **_step_inputs(2, 30, 1, 4, 64, 5))
+    assert not res.valid() and int(res.maps.pages_used) == 2
+    assert table.tolist() == [[1, 2, 5], [3, 4, -1]]
+    assert not res.out.isnan().any() and not res.lse.isnan().any()
+    assert (res.maps.slots[30:] == -1).all() and (res.maps.slots[:30] >= 0).all()
