@@ -52,6 +52,15 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def _has_torch() -> bool:
+    """The library builds and runs without torch; the binding is torch's own entry."""
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return False
+    return True
+
+
 def _torch_stamp() -> str:
     """What the binding was compiled against: torch's version and Python's."""
     import torch
@@ -150,7 +159,8 @@ def o0_units() -> list:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    lib_ok, binding_ok = not force and up_to_date(), not force and binding_up_to_date()
+    lib_ok = not force and up_to_date()
+    binding_ok = not _has_torch() or (not force and binding_up_to_date())
     if lib_ok and binding_ok:
         return LIB
     os.makedirs(BUILD, exist_ok=True)

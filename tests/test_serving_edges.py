@@ -2,6 +2,7 @@
 with other layouts and lengths than a plain step's (the operators themselves:
 test_serving_ops.py)."""
 import os
+import subprocess
 import sys
 import types
 
@@ -506,3 +507,20 @@ def test_step_without_enough_pages_reads_no_other_requests(cuda):
     assert table.tolist() == [[1, 2, 5], [3, 4, -1]]
     assert not res.out.isnan().any() and not res.lse.isnan().any()
     assert (res.maps.slots[30:] == -1).all() and (res.maps.slots[:30] >= 0).all()
+
+
+# ---------------------------------------------------------------------------
+# the library without torch
+# ---------------------------------------------------------------------------
+
+def test_the_library_builds_and_loads_without_torch(lib):
+    """As before there was a binding for torch tensors: the C ABI through ctypes needs
+    none of it."""
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "from sparse_attention_indexer_02_gb300 import build\n"
+            "build.build()\n"
+            "import sparse_attention_indexer_02_gb300 as qsa\n"
+            "assert qsa.abi_version() == 1 and qsa.status_string(1)\n")
+    root = os.path.dirname(qbuild.PKG)
+    res = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr[-2000:]
