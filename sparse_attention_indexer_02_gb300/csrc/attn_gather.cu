@@ -10,7 +10,7 @@
 //
 // What bounds it is the key/value bytes: HBM for a decode step, whose 16 or 32
 // query rows do at most 32 flop a byte (9 requests x 4 rows at 64-128K tokens:
-// 486 us, 7.1 TB/s), random 256-byte rows of HBM for selected decode (16 x 8256
+// 485 to 501 us, 6.9 to 7.1 TB/s), random 256-byte rows of HBM for selected decode (16 x 8256
 // keys: 50 us, of which copies alone are 49), the consumers' chain of steps for
 // selected chunks, whose rows come from L2 (512 rows x 2148 keys: 115 us; copies
 // alone 81).  So the kernel is a stream first.  Eight consumer warps work on 16

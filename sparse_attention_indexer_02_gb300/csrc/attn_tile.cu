@@ -14,9 +14,10 @@
 //
 // TMEM is full: S/P and O of both streams are 2 * 128 + 2 * D columns.
 // What bounds a chunk is the tensor core (4 * D flop a row and key): 8192 new
-// tokens at 32768, 32 heads of 128, take 2080 us, 1850 TFLOP/s, 0.97 of the
-// measured bf16 rate (back to back 2620, under the power limit).  The
-// exponentials are half its time.  The two streams exist to keep it busy: the
+// tokens at 32768, 32 heads of 128, take 2090 to 2170 us alone, 1775 to 1840
+// TFLOP/s, 0.93 to 0.97 of the measured bf16 rate, and 2550 to 2660 back to back,
+// 1450 to 1510 TFLOP/s, under the power limit (a library product keeps 1733
+// there).  The exponentials are half its time.  The two streams exist to keep it busy: the
 // softmax of one runs while the MMAs of the other do.  Two tiles on one key
 // tile also halve what L2 has to deliver, 64 KB for 2048 cycles of MMA.
 //
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kNT, 1)
   if (threadIdx.x == 0) p.meta[c * kMetaWords] = 0;
 
   // Registers: 384 threads of 168 at launch, of which the first four warps
-  // leave some to the softmax warps (128 * 96 + 256 * 200 are less).
+  // leave some to the softmax warps (128 * 72 + 256 * 216 is the same sum).
   if (s.u0 < s.u1) {
     if (warp == 0) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
