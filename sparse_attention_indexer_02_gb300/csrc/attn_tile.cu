@@ -485,7 +485,11 @@ __global__ void __launch_bounds__(kNT, 1)
         if (n > 0) {
           const int tk = row / p.group;
           const int32_t lim = min(max(it.pos0 + st * tpt + tk + 1, 0), it.keys);  // keys [0, lim) are seen
-          float m = -INFINITY, l = 0.0f;  // m in units of S
+          // m in units of S.  Rows of no token (the tile's rows past its tokens, whose q is
+          // whatever shared memory held) ask for no raise: it would move the warp's other rows.
+          const bool live = tk < n && row < tpt * p.group;
+          const float above = live ? raise : INFINITY;
+          float m = live ? -INFINITY : 0.0f, l = 0.0f;
           for (int j = ua; j < uz; ++j, ++tiles) {
             ok = __all_sync(0xffffffffu, wait_phase(&s_full[st], tiles & 1u, abort_flag, p.fault));
             if (!ok) break;
@@ -578,7 +582,7 @@ __global__ void __launch_bounds__(kNT, 1)
               max_of(3);
               const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
               if (again ||
-                  !__any_sync(0xffffffffu, tile_top > m + raise || (m == -INFINITY && tile_top > m)))
+                  !__any_sync(0xffffffffu, tile_top > m + above || (m == -INFINITY && tile_top > m)))
                 break;
               const float mn = fmaxf(m, tile_top);
               const float f = mn == -INFINITY ? 1.0f : ex2((m - mn) * sc);
@@ -609,7 +613,6 @@ __global__ void __launch_bounds__(kNT, 1)
           if (ok) {
             ptx::tc_fence_after();
             const int c0 = it.c0, c1 = it.c1;
-            const bool live = tk < n && row < tpt * p.group;
             const int64_t qrow = it.row0 + st * tpt + tk;
             const int head = it.head0 + (row - tk * p.group);
             if (c0 == c1) {

@@ -168,6 +168,24 @@ def test_selected_attention_does_not_see_missing_pages(cuda, local):
 
 
 # ---------------------------------------------------------------------------
+# tiles with rows of no token
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("group,D,pt", [(7, 64, 8), (20, 128, 64), (5, 128, 32)])
+def test_tile_rows_of_no_token_change_nothing(cuda, group, D, pt):
+    """Query heads that do not fill a tile's 128 rows: what the rest holds (another
+    call's queries, small or large) leaves every bit of the output as it was."""
+    pr = Problem([(200, 200), (513, 430), (64, 64), (90, 1)], 2, group, D, pt, "fp16", seed=group)
+    want = pr.run(form=_abi.ATTN_TILE)
+    for spread in (0.01, 2.0, 30.0):
+        other = Problem([(400, 300)] * 4, 2, 1, D, pt, "fp16", seed=1, spread=spread)
+        other.run(form=_abi.ATTN_TILE)
+        got = pr.run(form=_abi.ATTN_TILE)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ---------------------------------------------------------------------------
 # some requests of a larger batch
 # ---------------------------------------------------------------------------
 
