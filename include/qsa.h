@@ -601,6 +601,23 @@ qsa_status qsa_paged_attention(const qsa_attn_desc* desc, const void* q, const v
                                const int32_t* selected, void* out, float* lse, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/*
+ * qsa_paged_attention_window - qsa_paged_attention over a sliding window.
+ *
+ * A row at position p sees the tokens j <= p with j > p - window (the last
+ * `window` tokens, its own among them) or j < sink_tokens (the first tokens,
+ * which stay visible), window >= 1, sink_tokens >= 0; nothing else changes.
+ * num_selected and local_tokens are 0.  Table entries of pages that no row of the
+ * call sees may hold anything, so pages behind the window can be freed; cache
+ * contents no row sees are never used, whatever they hold.  Time and bytes
+ * follow the window, not seq_lens.  form and workspace as there
+ * (qsa_paged_attention_workspace, qsa_plan_attention).
+ */
+qsa_status qsa_paged_attention_window(const qsa_attn_desc* desc, int32_t window, int32_t sink_tokens, const void* q,
+                                      const void* k_cache, const void* v_cache, const int32_t* block_table,
+                                      const int32_t* query_start, const int32_t* seq_lens, void* out, float* lse,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
 /* Workspace bytes of a qsa_paged_attention call (host only): the unfinished
  * parts of the key splits, two a CTA, so independent of the lengths. */
 qsa_status qsa_paged_attention_workspace(const qsa_attn_desc* desc, size_t* bytes);
@@ -610,6 +627,138 @@ qsa_status qsa_paged_attention_workspace(const qsa_attn_desc* desc, size_t* byte
  * selected and pages hold 8, 16, 32, 64 or a multiple of 128 tokens; else
  * gathered rows. */
 qsa_status qsa_plan_attention(const qsa_attn_desc* desc, int32_t* form);
+
+/* ---------------------------------------------------------------------------
+ * Around a layer's attention and after the logits:
+ *
+ *   qsa_rotate_heads       queries and keys normalised head by head and rotated
+ *                          by their positions;
+ *   qsa_rotate_store_kv    the same, keys and values into the paged cache;
+ *   qsa_verify_drafts      drafted tokens against the target's probabilities.
+ *
+ * Like the serving operators above, these calls read nothing before the kernel
+ * ahead of them in the stream has completed.
+ * ------------------------------------------------------------------------- */
+
+/* Which elements of the rotated part form a pair. */
+typedef enum qsa_rotary_layout {
+  QSA_ROTARY_HALF = 0, /* i and i + rot_dim / 2 */
+  QSA_ROTARY_PAIRS = 1 /* 2 i and 2 i + 1       */
+} qsa_rotary_layout;
+
+typedef enum qsa_head_norm { QSA_NORM_NONE = 0, QSA_NORM_RMS = 1, QSA_NORM_LAYER = 2 } qsa_head_norm;
+
+/* Shape of one rotation (host values). */
+typedef struct qsa_rotary_desc {
+  int32_t dtype;       /* qsa_half_dtype of the rows                              */
+  int32_t head_dim;    /* D: a multiple of 8, 8..256                              */
+  int32_t rot_dim;     /* R: elements of a head that are rotated, even, 2..D      */
+  int32_t rot_offset;  /* the first of them, 0..D - R; even in the pairs layout   */
+  int32_t layout;      /* qsa_rotary_layout                                       */
+  int32_t norm;        /* qsa_head_norm                                           */
+  int32_t weight_f32;  /* weights and biases: 0 in the rows' type, 1 fp32         */
+  int32_t reserved;    /* 0                                                       */
+  float eps;           /* with a norm: finite, >= 0                               */
+  float magnitude;     /* cosines and sines are multiplied by it: finite          */
+  int64_t num_tokens;  /* T, 0..2^31-1                                            */
+} qsa_rotary_desc;
+
+/* Rows of heads: head h of token t starts at (const char*)x + t*x_row_stride +
+ * h*x_head_stride, its elements are contiguous; the output alike.  Strides are
+ * bytes, positive multiples of 16; x and out 16-byte aligned device pointers.
+ * out may be x itself (same strides); else it must not overlap an input. */
+typedef struct qsa_head_rows {
+  const void* x;
+  void* out;           /* qsa_rotate_store_kv's k: NULL, the cache takes it       */
+  const void* weight;  /* [D] device, NULL: ones (norm none: NULL)                */
+  const void* bias;    /* [D] device, NULL: zeros (layer norm only)               */
+  int64_t x_row_stride, x_head_stride, out_row_stride, out_head_stride;
+  int32_t num_heads;   /* 1..65536                                                */
+  int32_t reserved;    /* 0                                                       */
+} qsa_head_rows;
+
+/*
+ * qsa_rotate_heads - head norms and rotary positions of q and k in one pass.
+ *
+ * For every token t with positions[t] >= 0 and every head x of it:
+ *   n = x,  x w / sqrt(mean(x^2) + eps)  or  (x - mean) w / sqrt(var + eps) + b
+ * over all D elements, and then for i < R / 2 the pair (lo, hi) of the rotated
+ * part, with a = positions[t] * f_i:
+ *   lo' = m (lo cos a - hi sin a),   hi' = m (hi cos a + lo sin a);
+ * elements beside the rotated part stay n (without a norm: their bits).  All in
+ * fp32, rounded to the rows' type once.  Rows with a negative position are
+ * padding: neither read nor written.
+ *
+ * freqs: device uint64 [R / 2], f_i / (2 pi) in units of 2^-64, modulo 2^64: the
+ * angle of a position is exact modulo a turn but for that rounding.  positions:
+ * device int32 [T].  k may be NULL (q alone); q and k have the same tokens.
+ * num_tokens 0 launches nothing.
+ */
+qsa_status qsa_rotate_heads(const qsa_rotary_desc* desc, const qsa_head_rows* q, const qsa_head_rows* k,
+                            const int32_t* positions, const uint64_t* freqs, void* stream);
+
+/*
+ * qsa_rotate_store_kv - qsa_rotate_heads with the stores of qsa_store_paged_kv:
+ * the rotated keys go to their cache slots instead of k->out (which is NULL),
+ * the values v (row t, head h at (const char*)v + t*v_row_stride +
+ * h*v_head_stride) to the value slots as they are.  kv describes the caches:
+ * its dtype and head_dim are desc's, its num_kv_heads k->num_heads.  Rows whose
+ * slot is outside the cache store nothing (their q is still rotated); rows with
+ * a negative position are padding altogether.
+ */
+qsa_status qsa_rotate_store_kv(const qsa_rotary_desc* desc, const qsa_head_rows* q, const qsa_head_rows* k,
+                               const int32_t* positions, const uint64_t* freqs, const qsa_kv_desc* kv, const void* v,
+                               int64_t v_row_stride, int64_t v_head_stride, const int64_t* slots, void* k_cache,
+                               void* v_cache, void* stream);
+
+/* Element type of probabilities. */
+typedef enum qsa_probs_dtype { QSA_PROBS_F32 = 0, QSA_PROBS_BF16 = 1, QSA_PROBS_F16 = 2 } qsa_probs_dtype;
+
+/* Shape of one qsa_verify_drafts call (host values); strides in elements. */
+typedef struct qsa_verify_desc {
+  int32_t num_requests;  /* B, 0..65536                                             */
+  int32_t max_drafts;    /* K, 0..1024: drafts a request may bring                  */
+  int32_t vocab;         /* V, 1..2^30                                              */
+  int32_t dtype;         /* qsa_probs_dtype                                         */
+  int64_t target_request_stride, target_row_stride; /* >= 0                         */
+  int64_t draft_request_stride, draft_row_stride;   /* >= 0; without draft_probs 0  */
+} qsa_verify_desc;
+
+/*
+ * qsa_verify_drafts - acceptance of drafted tokens and the token after them.
+ *
+ * Request b brings n = num_drafts[b] (clamped to [0, K]; num_drafts NULL: K)
+ * drafted tokens x_i = draft_tokens[b][i].  Row i of its probabilities is that
+ * of the target (and of the draft) for the token at place i, given the drafts
+ * before it; the target has one row more, for the token after the last draft.
+ * With u = uniforms[b], p_i the target's and q_i the draft's probabilities
+ * (draft_probs NULL: drafts are certain, q_i(x_i) = 1):
+ *   draft i is accepted while u[i] q_i(x_i) < p_i(x_i), compared exactly; a draft
+ *   outside [0, V) is refused.  a is the number accepted.
+ *   The next token is the smallest j with sum_{l <= j} w_l > u[K] sum_l w_l,
+ *   where w = max(p_a - q_a, 0) if draft a was refused (all zero: p_a), p_n else.
+ * out_tokens[b]: the a accepted drafts, the next token, then -1;
+ * num_accepted[b] = a; next_lens[b] = max(context_lens[b], 0) + 1 + a: the tokens
+ * the cache holds that count, for a step that brought one token and the drafts
+ * (saturates at 2^31-1; both pointers or neither).
+ *
+ * Probabilities are clamped to [0, 1] (NaN: 0), those of a row add up to 8 at
+ * most (else the next token is unspecified, in range).  Weights count in units
+ * of 2^-60, so sums are exact and the result does not depend on their order.
+ * u outside [0, 1) is taken as the nearest inside (NaN: 0).  No weight at all:
+ * the next token is -1.  Rows past n (target) and n - 1 (draft) may hold
+ * anything; so may draft_tokens past n.
+ *
+ * Device pointers: target_probs [B][K + 1][V] and draft_probs [B][K][V] of the
+ * dtype, rows contiguous, element-aligned (16-byte aligned rows are read faster);
+ * draft_tokens int32 [B][K]; uniforms fp32 [B][K + 1]; num_drafts and
+ * context_lens int32 [B]; out_tokens int32 [B][K + 1], num_accepted and next_lens
+ * int32 [B].  Outputs do not overlap inputs, but next_lens may be context_lens.
+ */
+qsa_status qsa_verify_drafts(const qsa_verify_desc* desc, const int32_t* draft_tokens, const int32_t* num_drafts,
+                             const void* target_probs, const void* draft_probs, const float* uniforms,
+                             const int32_t* context_lens, int32_t* out_tokens, int32_t* num_accepted,
+                             int32_t* next_lens, void* stream);
 
 /* QSA_ABI_VERSION of the loaded library. */
 int32_t qsa_abi_version(void);

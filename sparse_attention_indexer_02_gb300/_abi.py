@@ -29,11 +29,15 @@ EXPORTED = ("qsa_paged_mqa_logits", "qsa_paged_mqa_logits_ragged", "qsa_paged_mq
             "qsa_plan_variant_ex", "qsa_force_variant",
             "qsa_last_variant", "qsa_status_string", "qsa_last_error", "qsa_abi_version", "qsa_device_status",
             "qsa_page_stream", "qsa_build_page_maps", "qsa_store_paged_kv", "qsa_store_index_keys",
-            "qsa_paged_attention", "qsa_paged_attention_workspace", "qsa_plan_attention")
+            "qsa_paged_attention", "qsa_paged_attention_window", "qsa_paged_attention_workspace", "qsa_plan_attention",
+            "qsa_rotate_heads", "qsa_rotate_store_kv", "qsa_verify_drafts")
 
 HALF_BF16, HALF_F16 = 0, 1
 ATTN_AUTO, ATTN_GATHER, ATTN_TILE = 0, 1, 2
 ATTN_COUNTER_BYTES = 640
+ROTARY_HALF, ROTARY_PAIRS = 0, 1
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
+PROBS_F32, PROBS_BF16, PROBS_F16 = 0, 1, 2
 FAULT_ATTENTION = 8  # device_status: an attention launch gave up on a wait
 
 
@@ -84,6 +88,24 @@ class AttnDesc(ctypes.Structure):
                [(n, ctypes.c_int64) for n in ("num_tokens", "table_stride", "q_token_stride", "q_head_stride",
                                               "out_token_stride", "out_head_stride")] + \
                [("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "head_dim", "rot_dim", "rot_offset", "layout", "norm",
+                                              "weight_f32", "reserved")] + \
+               [("eps", ctypes.c_float), ("magnitude", ctypes.c_float), ("num_tokens", ctypes.c_int64)]
+
+
+class HeadRows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "out", "weight", "bias")] + \
+               [(n, ctypes.c_int64) for n in ("x_row_stride", "x_head_stride", "out_row_stride", "out_head_stride")] + \
+               [("num_heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class VerifyDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_requests", "max_drafts", "vocab", "dtype")] + \
+               [(n, ctypes.c_int64) for n in ("target_request_stride", "target_row_stride", "draft_request_stride",
+                                              "draft_row_stride")]
 
 
 _lib = None
@@ -145,6 +167,15 @@ def load_library():
         lib.qsa_store_index_keys.argtypes = [ptr(IndexCacheDesc), vp, i64, vp, i64, vp, vp, vp]
         lib.qsa_paged_attention.restype = ctypes.c_int
         lib.qsa_paged_attention.argtypes = [ptr(AttnDesc)] + [vp] * 10 + [sz, vp]
+        lib.qsa_paged_attention_window.restype = ctypes.c_int
+        lib.qsa_paged_attention_window.argtypes = [ptr(AttnDesc), i32, i32] + [vp] * 9 + [sz, vp]
+        lib.qsa_rotate_heads.restype = ctypes.c_int
+        lib.qsa_rotate_heads.argtypes = [ptr(RotaryDesc), ptr(HeadRows), ptr(HeadRows), vp, vp, vp]
+        lib.qsa_rotate_store_kv.restype = ctypes.c_int
+        lib.qsa_rotate_store_kv.argtypes = [ptr(RotaryDesc), ptr(HeadRows), ptr(HeadRows), vp, vp, ptr(KvDesc), vp, i64,
+                                            i64, vp, vp, vp, vp]
+        lib.qsa_verify_drafts.restype = ctypes.c_int
+        lib.qsa_verify_drafts.argtypes = [ptr(VerifyDesc)] + [vp] * 10
         lib.qsa_paged_attention_workspace.restype = ctypes.c_int
         lib.qsa_paged_attention_workspace.argtypes = [ptr(AttnDesc), ptr(sz)]
         lib.qsa_plan_attention.restype = ctypes.c_int
@@ -330,6 +361,38 @@ def paged_attention(desc: AttnDesc, q, k_cache, v_cache, block_table, query_star
     _check(load_library().qsa_paged_attention(
         ctypes.byref(desc), _addr(q), _addr(k_cache), _addr(v_cache), _addr(block_table), _addr(query_start),
         _addr(seq_lens), _addr(selected), _addr(out), _addr(lse), _addr(workspace), int(workspace_bytes),
+        _stream(stream)))
+
+
+def paged_attention_window(desc: AttnDesc, window: int, sink_tokens: int, q, k_cache, v_cache, block_table, query_start,
+                           seq_lens, out, lse, workspace, workspace_bytes: int, stream=None) -> None:
+    _check(load_library().qsa_paged_attention_window(
+        ctypes.byref(desc), int(window), int(sink_tokens), _addr(q), _addr(k_cache), _addr(v_cache), _addr(block_table),
+        _addr(query_start), _addr(seq_lens), _addr(out), _addr(lse), _addr(workspace), int(workspace_bytes),
+        _stream(stream)))
+
+
+def _rows(r: Optional[HeadRows]):
+    return None if r is None else ctypes.byref(r)
+
+
+def rotate_heads(desc: RotaryDesc, q: HeadRows, k: Optional[HeadRows], positions, freqs, stream=None) -> None:
+    _check(load_library().qsa_rotate_heads(ctypes.byref(desc), _rows(q), _rows(k), _addr(positions), _addr(freqs),
+                                           _stream(stream)))
+
+
+def rotate_store_kv(desc: RotaryDesc, q: HeadRows, k: HeadRows, positions, freqs, kv: KvDesc, v, v_row_stride: int,
+                    v_head_stride: int, slots, k_cache, v_cache, stream=None) -> None:
+    _check(load_library().qsa_rotate_store_kv(
+        ctypes.byref(desc), _rows(q), _rows(k), _addr(positions), _addr(freqs), ctypes.byref(kv), _addr(v),
+        int(v_row_stride), int(v_head_stride), _addr(slots), _addr(k_cache), _addr(v_cache), _stream(stream)))
+
+
+def verify_drafts(desc: VerifyDesc, draft_tokens, num_drafts, target_probs, draft_probs, uniforms, context_lens,
+                  out_tokens, num_accepted, next_lens, stream=None) -> None:
+    _check(load_library().qsa_verify_drafts(
+        ctypes.byref(desc), _addr(draft_tokens), _addr(num_drafts), _addr(target_probs), _addr(draft_probs),
+        _addr(uniforms), _addr(context_lens), _addr(out_tokens), _addr(num_accepted), _addr(next_lens),
         _stream(stream)))
 
 

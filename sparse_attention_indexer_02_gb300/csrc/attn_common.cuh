@@ -66,6 +66,27 @@ __device__ __forceinline__ int32_t keys_of(const AttnParams& p, const Request& r
 __device__ __forceinline__ int32_t units_of(int32_t keys) { return max(1, (keys + kUnit - 1) / kUnit); }
 __device__ __forceinline__ int32_t item_units(const AttnParams& p, int32_t keys) { return units_of(keys) + p.item_cost; }
 
+// ---- windowed calls (WIN): a row at position p sees the keys j <= p with
+// p - window < j or j < sinks.  The keys from the sinks' end to the window of the
+// item's first token are skipped: place `at` of an item's units holds key `at`
+// before sink_span and key at + skip from there on.  Both ends are multiples of
+// win_align (1: gathered rows, which lie anywhere; a tile of 128 keys otherwise).
+
+// First key of the window of the token at position pos.
+__device__ __forceinline__ int32_t window_from(const AttnParams& p, int32_t pos) {
+  return max(0, max(pos, -1) + 1 - p.window);
+}
+template <bool WIN>
+__device__ __forceinline__ int32_t skip_of(const AttnParams& p, int32_t pos0, int32_t keys) {
+  if (!WIN) return 0;
+  const int32_t up = p.win_align - 1;
+  return max(0, min(window_from(p, pos0) & ~up, (keys + up) & ~up) - p.sink_span);
+}
+template <bool WIN>
+__device__ __forceinline__ int32_t key_at(const AttnParams& p, int32_t at, int32_t skip) {
+  return !WIN || at < p.sink_span ? at : at + skip;
+}
+
 // a / b of non-negative values; in 32 bits when they allow it (a 64-bit
 // division is some hundred instructions).
 __device__ __forceinline__ int64_t div_nn(int64_t a, int64_t b) {
@@ -76,19 +97,22 @@ __device__ __forceinline__ int64_t div_nn(int64_t a, int64_t b) {
 __device__ __forceinline__ int32_t tiles_of(const AttnParams& p, int32_t n) { return (n + p.tpi - 1) / p.tpi; }
 
 // Units of tile t of a request: of the tokens [t * tpi, (t + 1) * tpi).
+template <bool WIN>
 __device__ __forceinline__ int32_t tile_units(const AttnParams& p, const Request& r, int32_t t) {
-  return item_units(p, keys_of(p, r, min((t + 1) * p.tpi, r.n)));
+  const int32_t keys = keys_of(p, r, min((t + 1) * p.tpi, r.n));
+  return item_units(p, keys - skip_of<WIN>(p, r.pos0 + t * p.tpi, keys));
 }
 
 // Units of one head of each lane's request (n = 0: none), by the whole warp: a
 // lane adds up a few tiles itself, many are shared out over the lanes.
+template <bool WIN>
 __device__ __forceinline__ int64_t head_units(const AttnParams& p, const Request& r) {
   constexpr int32_t kAlone = 4;
   const int lane = (int)threadIdx.x & 31;
   const int32_t tiles = tiles_of(p, r.n);
   int64_t u = 0;
   if (tiles <= kAlone)
-    for (int32_t t = 0; t < tiles; ++t) u += tile_units(p, r, t);
+    for (int32_t t = 0; t < tiles; ++t) u += tile_units<WIN>(p, r, t);
   uint32_t many = __ballot_sync(0xffffffffu, tiles > kAlone);
   while (many) {
     const int src = __ffs(many) - 1;
@@ -97,7 +121,7 @@ __device__ __forceinline__ int64_t head_units(const AttnParams& p, const Request
     q.n = __shfl_sync(0xffffffffu, r.n, src);
     q.pos0 = __shfl_sync(0xffffffffu, r.pos0, src);
     int64_t part = 0;
-    for (int32_t t = lane; t < tiles_of(p, q.n); t += 32) part += tile_units(p, q, t);
+    for (int32_t t = lane; t < tiles_of(p, q.n); t += 32) part += tile_units<WIN>(p, q, t);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
     if (lane == src) u = part;
@@ -111,6 +135,7 @@ struct Item {
   int32_t row0;      // row of q of the first token
   int32_t pos0;      // position of the first token
   int32_t keys;      // keys the last token sees
+  int32_t skip;      // windowed calls: keys skipped behind the sinks
   int64_t s0, s1;    // the item's units in the call's list
 };
 
@@ -164,6 +189,7 @@ struct ItemInfo {
   int32_t gs, head0;   // query heads of its virtual head
   int32_t c0, c1;      // the CTAs that have a part of it
   int32_t last;        // of this CTA
+  int32_t skip;
 };
 
 struct SchedShared {
@@ -186,7 +212,7 @@ struct Start {
 // lane a request.  More: NT requests a round, a thread a request, ordered by a
 // block scan, and the thread whose request holds the CTA's first unit says so.
 // Up to NT requests the second pass works on what the first has in registers.
-template <int NT>
+template <int NT, bool WIN>
 __device__ __forceinline__ Schedule make_schedule(const AttnParams& p, SchedShared& sh, Start& at) {
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = p.num_requests;
@@ -202,7 +228,7 @@ __device__ __forceinline__ Schedule make_schedule(const AttnParams& p, SchedShar
   if (B <= 32) {
     Request r = {0, 0, 0};
     if (lane < B) r = request_of(p, lane);
-    const int64_t head = head_units(p, r), mine = head * p.hv, incl = scan(mine);
+    const int64_t head = head_units<WIN>(p, r), mine = head * p.hv, incl = scan(mine);
     s.share_out(__shfl_sync(0xffffffffu, incl, 31), p.min_shift);
     const uint32_t here = __ballot_sync(0xffffffffu, incl - mine <= s.u0 && s.u0 < incl);
     const int src = here ? __ffs(here) - 1 : 0;
@@ -219,7 +245,7 @@ __device__ __forceinline__ Schedule make_schedule(const AttnParams& p, SchedShar
   auto round = [&](int b0) {
     Request r = {0, 0, 0};
     if (b0 + tid < B) r = request_of(p, b0 + tid);
-    head = head_units(p, r);
+    head = head_units<WIN>(p, r);
     const int64_t mine = head * p.hv, incl = scan(mine);
     if (lane == 31) sh.warp_sum[warp] = incl;
     __syncthreads();
@@ -261,6 +287,7 @@ __device__ __forceinline__ Schedule make_schedule(const AttnParams& p, SchedShar
 
 // Walks the items of the list from the one that holds unit u0; made and moved
 // by whole warps.
+template <bool WIN>
 struct Walker {
   const AttnParams& p;
   Item it;
@@ -277,7 +304,7 @@ struct Walker {
     int64_t s = u0 - rem;  // the head's first unit
     const int32_t tiles = tiles_of(p, r.n);
     for (int32_t t0 = 0;; t0 += 32) {  // 32 tiles at a time: the one that holds the unit
-      const int32_t u = t0 + lane < tiles ? tile_units(p, r, t0 + lane) : 0;
+      const int32_t u = t0 + lane < tiles ? tile_units<WIN>(p, r, t0 + lane) : 0;
       int32_t incl = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -309,6 +336,7 @@ struct Walker {
     it.row0 = r.first + it.i0;
     it.pos0 = r.pos0 + it.i0;
     it.keys = keys_of(p, r, it.i0 + it.n);
+    it.skip = skip_of<WIN>(p, it.pos0, it.keys);
   }
   // To the next item; there is one (its first unit is it.s1).
   __device__ __forceinline__ void next() {
@@ -323,7 +351,7 @@ struct Walker {
     }
     set();
     it.s0 = it.s1;
-    it.s1 += item_units(p, it.keys);
+    it.s1 += item_units(p, it.keys - it.skip);
   }
 };
 

@@ -39,6 +39,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "attn_common.cuh"
 
 namespace qsa {
@@ -158,10 +160,11 @@ __device__ __forceinline__ Item selected_item(const AttnParams& p, int64_t u, in
   it.n = t >= r.first && t < r.first + r.n ? 1 : 0;
   it.pos0 = it.n > 0 ? r.pos0 + (t - r.first) : -1;
   it.keys = min(max(it.pos0 + 1, 0), p.capacity);
+  it.skip = 0;
   return it;
 }
 
-template <bool F16, int D, int MT, bool SEL>
+template <bool F16, int D, int MT, bool SEL, bool WIN>
 __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const AttnParams p) {
   using L = Layout<D, MT>;
   constexpr int kProducers = Conf<MT>::kProducers, kNT = Conf<MT>::kNT;
@@ -206,21 +209,21 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
     s.share_out(rows * p.hv * sel_units, p.min_shift);
     __syncthreads();
   } else {
-    s = make_schedule<kNT>(p, sched_sh, at);
+    s = make_schedule<kNT, WIN>(p, sched_sh, at);
   }
   if (s.u0 >= s.u1) return;
   auto next = [&](Item& it) {
     if (SEL) {
       it = selected_item(p, it.s1, sel_units, it.b);
     } else {
-      Walker w(p, it);
+      Walker<WIN> w(p, it);
       w.next();
       it = w.it;
     }
   };
   Item it;
   if (SEL) it = selected_item(p, s.u0, sel_units, 0);
-  else it = Walker(p, at, s.u0).it;
+  else it = Walker<WIN>(p, at, s.u0).it;
   if (!first_part(p, s, it, next)) return;
   // Registers: 512 threads of 128 at launch, 256 * 72 + 256 * 176 are less; or
   // 384 of 168, of which 128 * 88 + 256 * 208 is the same sum.
@@ -249,7 +252,7 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
       const int32_t* table = p.block_table + (int64_t)it.b * p.table_stride;
       const int32_t* sel = SEL ? p.selected + (int64_t)it.row0 * p.num_selected : nullptr;
       const int32_t local0 = SEL ? it.pos0 + 1 - p.local_tokens : 0;  // first of the last tokens
-      const int32_t keys = it.keys;
+      const int32_t keys = it.keys, skip = it.skip, low0 = WIN ? window_from(p, it.pos0) : 0;
       auto col_of = [&](int32_t at) -> int32_t { return p.ratio_shift >= 0 ? at >> p.ratio_shift : at / p.ratio; };
       auto entry_of = [&](int j) -> int32_t {  // SEL: the column listed for the place, -1 none
         const int32_t at = place_of(j);
@@ -258,7 +261,10 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
       auto token_of = [&](int j, int32_t col) -> int32_t {  // the token of the place, -1 none
         const int32_t at = place_of(j);
         if (!in_share(j)) return -1;
-        if (!SEL) return at < keys ? at : -1;
+        if (!SEL) {
+          const int32_t key = key_at<WIN>(p, at, skip);
+          return key < keys && (!WIN || key < p.sinks || key >= low0) ? key : -1;
+        }
         int64_t t;
         if (at < sel_end) {
           t = (int64_t)col * p.ratio + (at - col_of(at) * p.ratio);
@@ -300,6 +306,7 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
         o->c0 = first_cta(s, it);
         o->c1 = last_cta(p, s, it);
         o->last = it.s1 >= s.u1;
+        o->skip = it.skip;
         ptx::mbar_arrive(&q_full[k & 1]);
       }
 
@@ -378,13 +385,18 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) ldsm4(qf[MT == 1 ? ks : 0], q_addr + ks * 32);
       }
-      int32_t lim[MT][2];  // keys [0, lim) are seen by the thread's rows
+      int32_t lim[MT][2], low[MT][2];  // keys [0, lim) are seen by the thread's rows (windowed: [low, lim) and the sinks)
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          lim[mt][h] = min(max(info.pos0 + 1 + (mt * 16 + h * 8 + (lane >> 2)) / gs, 0), info.keys);
+        {
+          const int32_t pos = info.pos0 + (mt * 16 + h * 8 + (lane >> 2)) / gs;
+          lim[mt][h] = min(max(pos + 1, 0), info.keys);
+          low[mt][h] = WIN ? window_from(p, pos) : 0;
+        }
       const int32_t all_see = min(max(info.pos0 + 1, 0), info.keys);
+      const int32_t low_all = WIN ? window_from(p, info.pos0 + info.n - 1) : 0;  // every row's window holds the keys from here
 
       float o[MT][D / 8][4], m[MT][2], l[MT][2];
 #pragma unroll
@@ -432,8 +444,9 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[0][e >> 2][e & 3] += y[0][e >> 2][e & 3];
           }
-          const int32_t key0 = j * kUnit + warp * kSlice;
-          if (vm != 0xFFFFu || (!SEL && key0 + kSlice > all_see)) {
+          const int32_t at0 = j * kUnit + warp * kSlice, key0 = key_at<WIN>(p, at0, info.skip);
+          if (vm != 0xFFFFu || (!SEL && key_at<WIN>(p, at0 + kSlice - 1, info.skip) + 1 > all_see) ||
+              (WIN && key0 < low_all)) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -441,7 +454,9 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const int c = n * 8 + (lane & 3) * 2 + (e & 1);
-                  const bool seen = ((vm >> c) & 1u) && (SEL || key0 + c < lim[mt][e >> 1]);
+                  const int32_t key = key_at<WIN>(p, at0 + c, info.skip);
+                  const bool seen = ((vm >> c) & 1u) && (SEL || key < lim[mt][e >> 1]) &&
+                                    (!WIN || key < p.sinks || key >= low[mt][e >> 1]);
                   if (!seen) x[mt][n][e] = -INFINITY;
                 }
           }
@@ -671,9 +686,9 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
   }
 }
 
-template <bool F16, int D, int MT, bool SEL>
+template <bool F16, int D, int MT, bool SEL, bool WIN>
 cudaError_t launch_t(const AttnParams& p, int device, int grid, cudaStream_t stream) {
-  auto kern = attn_gather_kernel<F16, D, MT, SEL>;
+  auto kern = attn_gather_kernel<F16, D, MT, SEL, WIN>;
   constexpr int smem = Layout<D, MT>::total;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(kern, smem, device, allowed);
@@ -693,9 +708,12 @@ cudaError_t launch_t(const AttnParams& p, int device, int grid, cudaStream_t str
 
 template <bool F16, int D>
 cudaError_t launch_d(const AttnParams& p, int mt, int device, int grid, cudaStream_t stream) {
-  if (p.num_selected > 0)
-    return mt == 1 ? launch_t<F16, D, 1, true>(p, device, grid, stream) : launch_t<F16, D, 2, true>(p, device, grid, stream);
-  return mt == 1 ? launch_t<F16, D, 1, false>(p, device, grid, stream) : launch_t<F16, D, 2, false>(p, device, grid, stream);
+  auto by_tiles = [&](auto sel, auto win) {
+    return mt == 1 ? launch_t<F16, D, 1, sel.value, win.value>(p, device, grid, stream)
+                   : launch_t<F16, D, 2, sel.value, win.value>(p, device, grid, stream);
+  };
+  if (p.num_selected > 0) return by_tiles(std::true_type{}, std::false_type{});
+  return p.window > 0 ? by_tiles(std::false_type{}, std::true_type{}) : by_tiles(std::false_type{}, std::false_type{});
 }
 
 }  // namespace
@@ -727,6 +745,8 @@ cudaError_t launch_attn_gather(AttnParams p, const qsa_attn_desc& d, uint8_t* wo
   p.tpi = p.num_selected > 0 ? 1 : 16 * mt / p.sub;
   p.min_shift = 0;
   p.item_cost = kItemCost;
+  p.win_align = 1;
+  p.sink_span = p.sinks;
   p.ratio_shift = -1;
   for (int sh = 0; sh < 31; ++sh)
     if ((1 << sh) == p.ratio) p.ratio_shift = sh;

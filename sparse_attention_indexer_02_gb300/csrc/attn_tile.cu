@@ -218,7 +218,7 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t a, uint32_t b, uin
       : "memory");
 }
 
-template <bool F16, int D>
+template <bool F16, int D, bool WIN>
 __global__ void __launch_bounds__(kNT, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map, const AttnParams p) {
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kNT, 1)
   ptx::grid_dep_launch();
   ptx::tc_fence_before();
   Start at;
-  const Schedule s = make_schedule<kNT>(p, sched_sh, at);  // with a CTA barrier
+  const Schedule s = make_schedule<kNT, WIN>(p, sched_sh, at);  // with a CTA barrier
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int tpt = p.tpi / 2;  // tokens a stream
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kNT, 1)
       const int box = min(p.page_tokens, kUnit);
       uint32_t r = 0, items = 0;
       bool ok = true;
-      Walker w(p, at, s.u0);
+      Walker<WIN> w(p, at, s.u0);
       const Item& it = w.it;
       const bool any = first_part(p, s, w.it, [&](Item&) { w.next(); });
       if (!any && lane == 0) {
@@ -311,6 +311,7 @@ __global__ void __launch_bounds__(kNT, 1)
           o.c0 = first_cta(s, it);
           o.c1 = last_cta(p, s, it);
           o.last = it.s1 >= s.u1;
+          o.skip = it.skip;
         }
         ++items;
         if (lane == 0) {
@@ -321,20 +322,25 @@ __global__ void __launch_bounds__(kNT, 1)
                                      it.hv * p.group, it.row0 + st * tpt, &q_bar[0]);
         }
         const int32_t* table = p.block_table + (int64_t)it.b * p.table_stride;
+        const int32_t low0 = WIN ? window_from(p, it.pos0) : 0;
+        // A box between the sinks and the window of every row: zeros are loaded in its place.
+        auto unseen = [&](int32_t t) { return WIN && t >= p.sinks && t + box <= low0; };
         auto page_at = [&](int j) -> int32_t {  // the page of the lane's box of key tile j
-          const int32_t t = j * kUnit + lane * box;
-          return j < uz && lane * box < kUnit && t < it.keys ? table[t / p.page_tokens] : 0;
+          const int32_t t = key_at<WIN>(p, j * kUnit, it.skip) + lane * box;
+          return j < uz && lane * box < kUnit && t < it.keys && !unseen(t) ? table[t / p.page_tokens] : 0;
         };
         int32_t page = page_at(ua);
         for (int j = ua; j < uz && ok; ++j) {
-          const int valid = min(kUnit, it.keys - j * kUnit);
+          const int32_t key0 = key_at<WIN>(p, j * kUnit, it.skip);
+          const int valid = min(kUnit, it.keys - key0);
           const int nb = valid > 0 ? (valid + box - 1) / box : 0;
           // past the pool's end the copies write zeros
-          const int32_t pg = page == kNoPage ? p.num_pages : min(max(page, 0), p.num_pages - 1);
+          const int32_t pg = page == kNoPage || unseen(key0 + lane * box) ? p.num_pages
+                                                                          : min(max(page, 0), p.num_pages - 1);
           const uint32_t missing = __reduce_or_sync(
               0xffffffffu, page == kNoPage ? ((1u << (box >> 3)) - 1u) << (lane * (box >> 3)) : 0u);
           page = page_at(j + 1);
-          const int off = (j * kUnit + lane * box) % p.page_tokens;
+          const int off = (key0 + lane * box) % p.page_tokens;
           for (int kv = 0; kv < 2 && ok; ++kv, ++r) {
             const int st = r % kStages;
             ok = __all_sync(0xffffffffu, wait_phase(&empty[st], ((r / kStages) & 1u) ^ 1u, abort_flag, p.fault));
@@ -392,6 +398,7 @@ __global__ void __launch_bounds__(kNT, 1)
         const ItemInfo& it = item_sh[items & 1u];
         if (!ok || it.a < 0) break;
         const int ua = it.a, uz = it.z, keys = it.keys, last_item = it.last;
+        const int skip = it.skip, low0 = WIN ? window_from(p, it.pos0) : 0;
         const int nst = it.n > tpt ? 2 : 1;
         ok = wwait(&full[stage], phase);
         if (!ok) break;
@@ -407,14 +414,31 @@ __global__ void __launch_bounds__(kNT, 1)
           if (!ok) break;
           advance();  // to the key tile of j + 1, if there is one
           const bool more = j + 1 < uz;
-          const int valid = max(0, min(kUnit, keys - j * kUnit));
+          const int key0 = key_at<WIN>(p, j * kUnit, skip);
+          const int valid = max(0, min(kUnit, keys - key0));
           const int steps = (valid + 15) / 16;
-          if (valid & 15) {  // zero the value rows between the last key and the product's end
+          auto zero_rows = [&](int r0, int rows) {
             uint8_t* v = smem + G::ring + vst * G::kTile;
-            const int rows = steps * 16 - valid;
             for (int i = lane; i < rows * 8 * G::kHalves; i += 32)
-              *reinterpret_cast<uint4*>(v + (i / (rows * 8)) * (kRows * 128) + valid * 128 + (i % (rows * 8)) * 16) =
+              *reinterpret_cast<uint4*>(v + (i / (rows * 8)) * (kRows * 128) + r0 * 128 + (i % (rows * 8)) * 16) =
                   make_uint4(0, 0, 0, 0);
+          };
+          bool zeroed = false;
+          if (valid & 15) {  // the value rows between the last key and the product's end
+            zero_rows(valid, steps * 16 - valid);
+            zeroed = true;
+          }
+          if (WIN && key0 + kUnit > p.sinks && key0 < low0) {
+            // those between the sinks and the first row's window, but for the boxes loaded as
+            // zeros: from the sinks' end to its box's, and from the window's box to its start
+            const int box = min(p.page_tokens, kUnit), end = min(low0 - key0, valid);
+            const int s0 = max(p.sinks - key0, 0), s1 = min((s0 + box - 1) / box * box, end);
+            const int w0 = max(end / box * box, s1);
+            if (s0 < s1) zero_rows(s0, s1 - s0);
+            if (w0 < end) zero_rows(w0, end - w0);
+            zeroed = true;
+          }
+          if (zeroed) {
             ptx::fence_proxy_async_smem();
             __syncwarp();
           }
@@ -485,6 +509,8 @@ __global__ void __launch_bounds__(kNT, 1)
         if (n > 0) {
           const int tk = row / p.group;
           const int32_t lim = min(max(it.pos0 + st * tpt + tk + 1, 0), it.keys);  // keys [0, lim) are seen
+          const int32_t low = WIN ? window_from(p, it.pos0 + st * tpt + tk) : 0;  // windowed: [low, lim) and the sinks
+          const int32_t skip = it.skip;
           // m in units of S.  Rows of no token (the tile's rows past its tokens, whose q is
           // whatever shared memory held) ask for no raise: it would move the warp's other rows.
           const bool live = tk < n && row < tpt * p.group;
@@ -522,8 +548,10 @@ __global__ void __launch_bounds__(kNT, 1)
             ptx::tmem_ld_done32(x[1]);
             ptx::tmem_ld32(t_s + 64, x[2]);  // on their way while the first half is worked on
             ptx::tmem_ld32(t_s + 96, x[3]);
-            const int seen = lim - j * kUnit;
-            const bool edge = __any_sync(0xffffffffu, seen < kUnit);
+            const int key0 = key_at<WIN>(p, j * kUnit, skip);
+            const int seen = lim - key0;
+            const int from = WIN ? low - key0 : 0, sink = WIN ? p.sinks - key0 : 0;  // [sink, from) is masked
+            const bool edge = __any_sync(0xffffffffu, seen < kUnit || (WIN && from > 0 && sink < kUnit));
             float top[4];
             uint64_t sum[2];
             // The causal edge and the end of the keys: one block, out of the way of the loop,
@@ -537,7 +565,7 @@ __global__ void __launch_bounds__(kNT, 1)
               for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                  if (q * 32 + i >= seen) x[q][i] = 0xFF800000u;
+                  if (q * 32 + i >= seen || (WIN && q * 32 + i >= sink && q * 32 + i < from)) x[q][i] = 0xFF800000u;
             }
             auto max_of = [&](int q) {
               float t[2] = {__uint_as_float(x[q][0]), __uint_as_float(x[q][1])};
@@ -741,10 +769,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
   if (warp == 0 && p.lse) p.lse[qrow * p.num_q_heads + head] = (M + log2f(L)) * kLn2;
 }
 
-template <bool F16, int D>
-cudaError_t launch_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p, int device,
+template <bool F16, int D, bool WIN>
+cudaError_t launch_w(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p, int device,
                      int grid, cudaStream_t stream) {
-  auto kern = attn_tile_kernel<F16, D>;
+  auto kern = attn_tile_kernel<F16, D, WIN>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(kern, Geo<D>::total, device, allowed);
   if (e != cudaSuccess) return e;
@@ -764,6 +792,13 @@ cudaError_t launch_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtenso
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_join_kernel<F16, D>, p);
+}
+
+template <bool F16, int D>
+cudaError_t launch_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p, int device,
+                     int grid, cudaStream_t stream) {
+  return p.window > 0 ? launch_w<F16, D, true>(qm, km, vm, p, device, grid, stream)
+                      : launch_w<F16, D, false>(qm, km, vm, p, device, grid, stream);
 }
 
 }  // namespace
@@ -822,6 +857,8 @@ cudaError_t launch_attn_tile(AttnParams p, const qsa_attn_desc& d, uint8_t* work
   p.tpi = 2 * tpt;
   p.min_shift = 1;
   p.item_cost = kItemCost;
+  p.win_align = kUnit;
+  p.sink_span = (p.sinks + kUnit - 1) / kUnit * kUnit;
   p.out32 = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.out_token_stride % 32 == 0 && p.out_head_stride % 32 == 0;
   const CUtensorMapDataType ty = f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap qm, km, vm;

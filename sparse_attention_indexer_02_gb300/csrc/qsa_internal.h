@@ -119,6 +119,40 @@ struct StoreIndexParams {
 };
 cudaError_t launch_store_index(const StoreIndexParams& p, cudaStream_t stream);
 
+// head_rotate.cuh: qsa_rotate_heads, qsa_rotate_store_kv.
+struct HeadRows {             // one of q, k, v; strides in bytes
+  const uint8_t* x;
+  uint8_t* out;               // null: into the cache
+  const void *weight, *bias;  // may be null
+  int64_t x_row, x_head, out_row, out_head;
+  int32_t heads;              // 0: not given
+};
+struct RotateParams {
+  HeadRows rows[3];
+  const int32_t* positions;
+  const uint64_t* freqs;
+  const int64_t* slots;       // null: no store
+  uint8_t *k_cache, *v_cache;
+  int64_t k_page_stride, k_token_stride, k_head_stride, v_page_stride, v_token_stride, v_head_stride;
+  int64_t num_tokens, num_slots;
+  int32_t page_tokens, head_dim, rot_dim, rot_offset, layout, norm, weight32;
+  int32_t per_block, blocks;  // passes a warp takes, and into how many warps that divides a token
+  float eps, inv_dim, magnitude;
+};
+cudaError_t launch_rotate_bf16(const RotateParams& p, cudaStream_t stream);
+cudaError_t launch_rotate_fp16(const RotateParams& p, cudaStream_t stream);
+
+// verify_drafts.cu: qsa_verify_drafts; strides in elements.
+struct VerifyParams {
+  const void *target, *draft;   // draft may be null
+  const int32_t *tokens, *num_drafts, *context_lens;  // the last two may be null
+  const float* uniforms;
+  int32_t *out_tokens, *num_accepted, *next_lens;     // next_lens may be null
+  int64_t target_request, target_row, draft_request, draft_row;
+  int32_t num_requests, max_drafts, vocab, dtype;
+};
+cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream);
+
 // attn_gather.cu, attn_tile.cu: qsa_paged_attention.
 struct AttnParams {
   const uint8_t *q, *k, *v;
@@ -141,6 +175,8 @@ struct AttnParams {
   int32_t out32;              // tile form: rows of out are 32-byte aligned
   int32_t min_shift;          // a CTA takes at least 2^min_shift units (fewer CTAs take part then)
   int32_t num_selected, ratio, ratio_shift, local_tokens;  // ratio_shift: log2, or -1
+  int32_t window, sinks;      // windowed calls: a row's last tokens and the first ones; 0 else
+  int32_t sink_span, win_align;  // sinks rounded up to win_align: places before the skipped keys
   int32_t near_rows;          // keys and values: equal strides, offsets below 2^36 bytes
   float scale_log2;           // scale * log2(e)
 };

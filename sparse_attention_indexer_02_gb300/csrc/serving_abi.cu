@@ -2,37 +2,13 @@
 // Declarations, argument meaning and error behaviour are in include/qsa.h.
 #include <math.h>
 
+#include "abi_checks.h"
 #include "qsa_internal.h"
 
 namespace {
 
+using namespace qsa::abi;
 using qsa::set_error;
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-qsa_status bad(const char* what) { return set_error(QSA_ERR_INVALID_ARG, "%s", what); }
-
-qsa_status launched(cudaError_t e, const char* what) {
-  if (e == cudaSuccess) return QSA_OK;
-  return set_error(QSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-bool stride_ok(int64_t s) { return s > 0 && s % 16 == 0; }
-
-qsa_status validate_kv(const qsa_kv_desc& d) {
-  if (d.dtype != QSA_HALF_BF16 && d.dtype != QSA_HALF_F16)
-    return set_error(QSA_ERR_INVALID_ARG, "unknown cache dtype %d", d.dtype);
-  if (d.num_pages < 1) return bad("num_pages < 1");
-  if (d.page_tokens < 1) return bad("page_tokens < 1");
-  if (d.num_kv_heads < 1) return bad("num_kv_heads < 1");
-  if (d.head_dim < 8 || d.head_dim > 1024 || d.head_dim % 8 != 0)
-    return set_error(QSA_ERR_INVALID_ARG, "head_dim must be a multiple of 8 in 8..1024 (got %d)", d.head_dim);
-  if (d.reserved != 0) return bad("kv.reserved must be 0");
-  if (!stride_ok(d.k_page_stride) || !stride_ok(d.k_token_stride) || !stride_ok(d.k_head_stride) ||
-      !stride_ok(d.v_page_stride) || !stride_ok(d.v_token_stride) || !stride_ok(d.v_head_stride))
-    return bad("cache strides must be positive multiples of 16 bytes");
-  return QSA_OK;
-}
 
 qsa_status validate_attn(const qsa_attn_desc* d) {
   if (!d) return bad("desc is NULL");
@@ -79,6 +55,78 @@ qsa_status plan_form(const qsa_attn_desc* d, int32_t* form) {
   const int64_t rows = toks * (d->num_q_heads / d->kv.num_kv_heads);
   *form = tile && rows > qsa::kTileAbove ? QSA_ATTN_TILE : QSA_ATTN_GATHER;
   return QSA_OK;
+}
+
+// window 0: every key up to a row's own is seen (or the selected ones).
+qsa_status attention(const qsa_attn_desc* d, int32_t window, int32_t sinks, const void* q, const void* k_cache,
+                     const void* v_cache, const int32_t* block_table, const int32_t* query_start,
+                     const int32_t* seq_lens, const int32_t* selected, void* out, float* lse, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  int32_t form = 0;
+  qsa_status st = plan_form(d, &form);
+  if (st != QSA_OK) return st;
+  if (d->num_selected > 0 && !selected && d->num_tokens > 0) return bad("num_selected > 0 needs the selected columns");
+  if (d->num_selected == 0 && selected) return bad("selected given with num_selected 0");
+  if (d->num_requests == 0 || d->num_tokens == 0) return QSA_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !query_start || !seq_lens || !out)
+    return bad("a required pointer is NULL");
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
+    return bad("q, the caches and out must be 16-byte aligned");
+  if (!aligned(block_table, 4) || !aligned(query_start, 4) || !aligned(seq_lens, 4) || !aligned(selected, 4) ||
+      !aligned(lse, 4))
+    return bad("a 4-byte pointer is misaligned");
+  const size_t need = form == QSA_ATTN_TILE ? qsa::attn_tile_workspace(d->kv.head_dim)
+                                            : qsa::attn_gather_workspace(d->kv.head_dim);
+  if (!workspace || workspace_bytes < need) return set_error(QSA_ERR_INVALID_ARG, "workspace below %zu bytes", need);
+  if (!aligned(workspace, 16)) return bad("workspace is not 16-byte aligned");
+  qsa::AttnParams p = {};
+  p.q = (const uint8_t*)q;
+  p.k = (const uint8_t*)k_cache;
+  p.v = (const uint8_t*)v_cache;
+  p.out = (uint8_t*)out;
+  p.lse = lse;
+  p.block_table = block_table;
+  p.query_start = query_start;
+  p.seq_lens = seq_lens;
+  p.selected = selected;
+  cudaError_t e = qsa::fault_word_address(&p.fault);
+  if (e != cudaSuccess) return launched(e, "fault word");
+  p.q_token_stride = d->q_token_stride;
+  p.q_head_stride = d->q_head_stride;
+  p.out_token_stride = d->out_token_stride;
+  p.out_head_stride = d->out_head_stride;
+  p.k_page_stride = d->kv.k_page_stride;
+  p.k_token_stride = d->kv.k_token_stride;
+  p.k_head_stride = d->kv.k_head_stride;
+  p.v_page_stride = d->kv.v_page_stride;
+  p.v_token_stride = d->kv.v_token_stride;
+  p.v_head_stride = d->kv.v_head_stride;
+  p.table_stride = d->table_stride;
+  p.num_requests = d->num_requests;
+  p.num_tokens = (int32_t)d->num_tokens;
+  p.num_q_heads = d->num_q_heads;
+  p.max_pages = d->max_pages;
+  p.num_pages = d->kv.num_pages;
+  p.page_tokens = d->kv.page_tokens;
+  p.page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if ((1 << s) == d->kv.page_tokens) p.page_shift = s;
+  const int64_t cap = (int64_t)d->max_pages * d->kv.page_tokens;
+  p.capacity = (int32_t)(cap < qsa::kMaxKeys ? cap : qsa::kMaxKeys);
+  p.group = d->num_q_heads / d->kv.num_kv_heads;
+  p.num_selected = d->num_selected;
+  p.ratio = d->ratio;
+  p.local_tokens = d->local_tokens;
+  p.window = window;
+  p.sinks = sinks < p.capacity ? sinks : p.capacity;
+  p.scale_log2 = d->scale * 1.4426950408889634f;
+  if (form == QSA_ATTN_TILE) {
+    const char* msg = nullptr;
+    e = qsa::launch_attn_tile(p, *d, (uint8_t*)workspace, (cudaStream_t)stream, &msg);
+    if (msg) return set_error(QSA_ERR_UNSUPPORTED, "%s", msg);
+    return launched(e, "attention (tile) launch");
+  }
+  return launched(qsa::launch_attn_gather(p, *d, (uint8_t*)workspace, (cudaStream_t)stream), "attention launch");
 }
 
 }  // namespace
@@ -232,69 +280,20 @@ qsa_status qsa_paged_attention(const qsa_attn_desc* d, const void* q, const void
                                const int32_t* block_table, const int32_t* query_start, const int32_t* seq_lens,
                                const int32_t* selected, void* out, float* lse, void* workspace,
                                size_t workspace_bytes, void* stream) {
-  int32_t form = 0;
-  qsa_status st = plan_form(d, &form);
-  if (st != QSA_OK) return st;
-  if (d->num_selected > 0 && !selected && d->num_tokens > 0) return bad("num_selected > 0 needs the selected columns");
-  if (d->num_selected == 0 && selected) return bad("selected given with num_selected 0");
-  if (d->num_requests == 0 || d->num_tokens == 0) return QSA_OK;
-  if (!q || !k_cache || !v_cache || !block_table || !query_start || !seq_lens || !out)
-    return bad("a required pointer is NULL");
-  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
-    return bad("q, the caches and out must be 16-byte aligned");
-  if (!aligned(block_table, 4) || !aligned(query_start, 4) || !aligned(seq_lens, 4) || !aligned(selected, 4) ||
-      !aligned(lse, 4))
-    return bad("a 4-byte pointer is misaligned");
-  const size_t need = form == QSA_ATTN_TILE ? qsa::attn_tile_workspace(d->kv.head_dim)
-                                            : qsa::attn_gather_workspace(d->kv.head_dim);
-  if (!workspace || workspace_bytes < need) return set_error(QSA_ERR_INVALID_ARG, "workspace below %zu bytes", need);
-  if (!aligned(workspace, 16)) return bad("workspace is not 16-byte aligned");
-  qsa::AttnParams p = {};
-  p.q = (const uint8_t*)q;
-  p.k = (const uint8_t*)k_cache;
-  p.v = (const uint8_t*)v_cache;
-  p.out = (uint8_t*)out;
-  p.lse = lse;
-  p.block_table = block_table;
-  p.query_start = query_start;
-  p.seq_lens = seq_lens;
-  p.selected = selected;
-  cudaError_t e = qsa::fault_word_address(&p.fault);
-  if (e != cudaSuccess) return launched(e, "fault word");
-  p.q_token_stride = d->q_token_stride;
-  p.q_head_stride = d->q_head_stride;
-  p.out_token_stride = d->out_token_stride;
-  p.out_head_stride = d->out_head_stride;
-  p.k_page_stride = d->kv.k_page_stride;
-  p.k_token_stride = d->kv.k_token_stride;
-  p.k_head_stride = d->kv.k_head_stride;
-  p.v_page_stride = d->kv.v_page_stride;
-  p.v_token_stride = d->kv.v_token_stride;
-  p.v_head_stride = d->kv.v_head_stride;
-  p.table_stride = d->table_stride;
-  p.num_requests = d->num_requests;
-  p.num_tokens = (int32_t)d->num_tokens;
-  p.num_q_heads = d->num_q_heads;
-  p.max_pages = d->max_pages;
-  p.num_pages = d->kv.num_pages;
-  p.page_tokens = d->kv.page_tokens;
-  p.page_shift = -1;
-  for (int s = 0; s < 31; ++s)
-    if ((1 << s) == d->kv.page_tokens) p.page_shift = s;
-  const int64_t cap = (int64_t)d->max_pages * d->kv.page_tokens;
-  p.capacity = (int32_t)(cap < qsa::kMaxKeys ? cap : qsa::kMaxKeys);
-  p.group = d->num_q_heads / d->kv.num_kv_heads;
-  p.num_selected = d->num_selected;
-  p.ratio = d->ratio;
-  p.local_tokens = d->local_tokens;
-  p.scale_log2 = d->scale * 1.4426950408889634f;
-  if (form == QSA_ATTN_TILE) {
-    const char* msg = nullptr;
-    e = qsa::launch_attn_tile(p, *d, (uint8_t*)workspace, (cudaStream_t)stream, &msg);
-    if (msg) return set_error(QSA_ERR_UNSUPPORTED, "%s", msg);
-    return launched(e, "attention (tile) launch");
-  }
-  return launched(qsa::launch_attn_gather(p, *d, (uint8_t*)workspace, (cudaStream_t)stream), "attention launch");
+  return attention(d, 0, 0, q, k_cache, v_cache, block_table, query_start, seq_lens, selected, out, lse, workspace,
+                   workspace_bytes, stream);
+}
+
+qsa_status qsa_paged_attention_window(const qsa_attn_desc* d, int32_t window, int32_t sink_tokens, const void* q,
+                                      const void* k_cache, const void* v_cache, const int32_t* block_table,
+                                      const int32_t* query_start, const int32_t* seq_lens, void* out, float* lse,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  if (!d) return bad("desc is NULL");
+  if (window < 1) return bad("window < 1");
+  if (sink_tokens < 0) return bad("sink_tokens < 0");
+  if (d->num_selected != 0 || d->local_tokens != 0) return bad("a window takes no selected columns (num_selected and local_tokens 0)");
+  return attention(d, window, sink_tokens, q, k_cache, v_cache, block_table, query_start, seq_lens, nullptr, out, lse,
+                   workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

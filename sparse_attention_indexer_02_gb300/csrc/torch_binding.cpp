@@ -374,10 +374,11 @@ at::Tensor attention_workspace(size_t bytes, const at::Tensor& like, cudaStream_
 }
 
 // (q, k_cache, v_cache, block_table, query_start, seq_lens, scale or None, max_new, selected or None, ratio,
-//  local_tokens, form, out or None, lse or None, return_lse, workspace or None) -> (status, out, lse or None)
+//  local_tokens, form, out or None, lse or None, return_lse, workspace or None, window, sink_tokens)
+//  -> (status, out, lse or None)
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    arity(n, 16);
+    arity(n, 18);
     const at::Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache"),
                      &bt = tensor(a[3], "block_table"), &qs = tensor(a[4], "query_start"),
                      &sl = tensor(a[5], "seq_lens");
@@ -409,6 +410,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     d.ratio = integer32(a[9], "ratio");
     d.local_tokens = integer32(a[10], "local_tokens");
     d.form = integer32(a[11], "form");
+    const int32_t window = integer32(a[16], "window"), sinks = integer32(a[17], "sink_tokens");
     d.num_tokens = T;
     d.table_stride = step_of(bt, 0);
     d.q_token_stride = 2 * step_of(q, 0);
@@ -451,10 +453,19 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       } else if (B > 0 && T > 0) {
         ws = attention_workspace(bytes, q, stream);
       }
-      st = qsa_paged_attention(&d, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), bt.data_ptr<int32_t>(),
-                               qs.data_ptr<int32_t>(), sl.data_ptr<int32_t>(), sel, out.data_ptr(),
-                               lse.defined() ? lse.data_ptr<float>() : nullptr,
-                               ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, stream);
+      float* const z = lse.defined() ? lse.data_ptr<float>() : nullptr;
+      void* const w = ws.defined() ? ws.data_ptr() : nullptr;
+      const size_t have = ws.defined() ? ws.nbytes() : 0;
+      if (window != 0 || sinks != 0) {
+        need(sel == nullptr, "a window takes no selected columns");
+        st = qsa_paged_attention_window(&d, window, sinks, q.data_ptr(), kc.data_ptr(), vc.data_ptr(),
+                                        bt.data_ptr<int32_t>(), qs.data_ptr<int32_t>(), sl.data_ptr<int32_t>(),
+                                        out.data_ptr(), z, w, have, stream);
+      } else {
+        st = qsa_paged_attention(&d, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), bt.data_ptr<int32_t>(),
+                                 qs.data_ptr<int32_t>(), sl.data_ptr<int32_t>(), sel, out.data_ptr(), z, w, have,
+                                 stream);
+      }
     }
     PyObject* r = PyTuple_New(3);
     if (!r) return nullptr;
@@ -470,6 +481,227 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// What of a call is fp32 where Python gives a number.
+float real32(PyObject* o, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    throw Refused(std::string(name) + " must be a number");
+  }
+  return (float)v;
+}
+
+// A weight or bias vector of head_dim entries: null when not given.  `f32`: -1
+// while none of the call's vectors has been seen.
+const void* head_vector(PyObject* o, const char* name, const at::Tensor& rows, const Place& place, int& f32) {
+  if (!given(o)) return nullptr;
+  const at::Tensor& t = tensor(o, name);
+  const int is32 = t.scalar_type() == at::kFloat ? 1 : 0;
+  if (!(is32 || t.scalar_type() == rows.scalar_type()) || t.dim() != 1 || t.size(0) != rows.size(2) ||
+      !t.is_contiguous())
+    throw Refused(std::string(name) + " must be a contiguous [head_dim] vector in the rows' type or fp32");
+  need(f32 < 0 || f32 == is32, "weights and biases must all be of one type");
+  f32 = is32;
+  place.also(t);
+  return t.data_ptr();
+}
+
+void head_rows(const at::Tensor& t, const at::Tensor& q, const char* name) {
+  if (t.dim() != 3 || t.scalar_type() != q.scalar_type() || t.size(0) != q.size(0) || t.size(2) != q.size(2) ||
+      step_of(t, 2) != 1)
+    throw Refused(std::string(name) + " must be [T, heads, head_dim] in q's type, last dimension contiguous");
+}
+
+// An output like `like`: the given tensor, or a new one.
+at::Tensor output_rows(PyObject* o, const char* name, const at::Tensor& like, const Place& place) {
+  if (!given(o)) return at::empty(like.sizes(), like.options());
+  const at::Tensor& t = tensor(o, name);
+  head_rows(t, like, name);
+  if (t.size(1) != like.size(1)) throw Refused(std::string(name) + " must have as many heads as its input");
+  place.also(t);
+  return t;
+}
+
+void strides_of(qsa_head_rows& r, const at::Tensor& x) {
+  r.x = x.data_ptr();
+  r.x_row_stride = 2 * step_of(x, 0);
+  r.x_head_stride = 2 * step_of(x, 1);
+  r.num_heads = size32(x.size(1), "heads");
+}
+
+// (q, k or None, positions, freqs, layout, offset, magnitude, norm, q_weight, k_weight, q_bias, k_bias, eps,
+//  q_out or None, k_out or None, v or None, slots, k_cache, v_cache) -> (status, q_out, k_out or None)
+// With v: keys and values go to the caches.
+PyObject* rotate_heads(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 19);
+    const at::Tensor &q = tensor(a[0], "q"), &pos = tensor(a[2], "positions"), &freqs = tensor(a[3], "freqs");
+    need(q.scalar_type() == at::kBFloat16 || q.scalar_type() == at::kHalf, "q must be bf16 or fp16");
+    head_rows(q, q, "q");
+    const int64_t T = q.size(0);
+    vec(pos, "positions", at::kInt, T);
+    vec(freqs, "freqs", at::kLong, -1);
+    const Place place(q);
+    place.also(pos), place.also(freqs);
+    qsa_rotary_desc d = {};
+    d.dtype = q.scalar_type() == at::kHalf ? QSA_HALF_F16 : QSA_HALF_BF16;
+    d.head_dim = size32(q.size(2), "head_dim");
+    need(freqs.size(0) < (1 << 20), "freqs is too long");
+    d.rot_dim = (int32_t)(2 * freqs.size(0));
+    d.layout = integer32(a[4], "layout");
+    d.rot_offset = integer32(a[5], "offset");
+    d.magnitude = real32(a[6], "magnitude");
+    d.norm = integer32(a[7], "norm");
+    d.eps = real32(a[12], "eps");
+    d.num_tokens = T;
+    qsa_head_rows rq = {}, rk = {};
+    int f32 = -1;
+    strides_of(rq, q);
+    rq.weight = head_vector(a[8], "q_weight", q, place, f32);
+    rq.bias = head_vector(a[10], "q_bias", q, place, f32);
+    const bool has_k = given(a[1]), stored = given(a[15]);
+    const at::Tensor* k = nullptr;
+    if (has_k) {
+      k = &tensor(a[1], "k");
+      head_rows(*k, q, "k");
+      place.also(*k);
+      strides_of(rk, *k);
+      rk.weight = head_vector(a[9], "k_weight", q, place, f32);
+      rk.bias = head_vector(a[11], "k_bias", q, place, f32);
+    } else {
+      need(!given(a[9]) && !given(a[11]) && !given(a[14]), "k_weight, k_bias and k_out need k");
+    }
+    d.weight_f32 = f32 == 1 ? 1 : 0;
+    at::Tensor q_out = output_rows(a[13], "q_out", q, place), k_out;
+    rq.out = q_out.data_ptr();
+    rq.out_row_stride = 2 * step_of(q_out, 0);
+    rq.out_head_stride = 2 * step_of(q_out, 1);
+    qsa_status st;
+    if (stored) {
+      need(has_k && !given(a[14]), "the store takes k, and its output is the cache");
+      const at::Tensor &v = tensor(a[15], "v"), &slots = tensor(a[16], "slots"), &kc = tensor(a[17], "k_cache"),
+                       &vc = tensor(a[18], "v_cache");
+      head_rows(v, q, "v");
+      need(v.size(1) == k->size(1), "v must have as many heads as k");
+      const qsa_kv_desc kv = kv_desc(kc, vc);
+      vec(slots, "slots", at::kLong, T);
+      place.also(v), place.also(slots), place.also(kc), place.also(vc);
+      st = qsa_rotate_store_kv(&d, &rq, &rk, pos.data_ptr<int32_t>(),
+                               reinterpret_cast<const uint64_t*>(freqs.data_ptr<int64_t>()), &kv, v.data_ptr(),
+                               2 * step_of(v, 0), 2 * step_of(v, 1), slots.data_ptr<int64_t>(), kc.data_ptr(),
+                               vc.data_ptr(), place.stream());
+    } else {
+      if (has_k) {
+        k_out = output_rows(a[14], "k_out", *k, place);
+        rk.out = k_out.data_ptr();
+        rk.out_row_stride = 2 * step_of(k_out, 0);
+        rk.out_head_stride = 2 * step_of(k_out, 1);
+      }
+      st = qsa_rotate_heads(&d, &rq, has_k ? &rk : nullptr, pos.data_ptr<int32_t>(),
+                            reinterpret_cast<const uint64_t*>(freqs.data_ptr<int64_t>()), place.stream());
+    }
+    PyObject* r = PyTuple_New(3);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, PyLong_FromLong(st));
+    PyTuple_SET_ITEM(r, 1, wrap(q_out));
+    if (k_out.defined()) {
+      PyTuple_SET_ITEM(r, 2, wrap(k_out));
+    } else {
+      Py_INCREF(Py_None);
+      PyTuple_SET_ITEM(r, 2, Py_None);
+    }
+    return r;
+  });
+}
+
+int32_t probs_dtype(const at::Tensor& t) {
+  if (t.scalar_type() == at::kFloat) return QSA_PROBS_F32;
+  if (t.scalar_type() == at::kBFloat16) return QSA_PROBS_BF16;
+  if (t.scalar_type() == at::kHalf) return QSA_PROBS_F16;
+  throw Refused("probabilities must be fp32, bf16 or fp16");
+}
+
+// (draft_tokens, target_probs, uniforms, draft_probs or None, num_drafts or None, context_lens or None,
+//  tokens or None, num_accepted or None, next_lens or None) -> (status, tokens, num_accepted, next_lens or None)
+PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 9);
+    const at::Tensor &tok = tensor(a[0], "draft_tokens"), &p = tensor(a[1], "target_probs"),
+                     &u = tensor(a[2], "uniforms");
+    need(tok.dim() == 2 && tok.scalar_type() == at::kInt && tok.is_contiguous(),
+         "draft_tokens must be a contiguous int32 [B, K] tensor");
+    const int64_t B = tok.size(0), K = tok.size(1);
+    need(p.dim() == 3 && p.size(0) == B && p.size(1) == K + 1 && step_of(p, 2) == 1,
+         "target_probs must be [B, K + 1, V], last dimension contiguous");
+    need(u.dim() == 2 && u.scalar_type() == at::kFloat && u.is_contiguous() && u.size(0) == B && u.size(1) == K + 1,
+         "uniforms must be a contiguous fp32 [B, K + 1] tensor");
+    const Place place(p);
+    place.also(tok), place.also(u);
+    qsa_verify_desc d = {};
+    d.num_requests = size32(B, "B");
+    d.max_drafts = size32(K, "K");
+    d.vocab = size32(p.size(2), "V");
+    d.dtype = probs_dtype(p);
+    d.target_request_stride = step_of(p, 0);
+    d.target_row_stride = step_of(p, 1);
+    const void* q = nullptr;
+    if (given(a[3])) {
+      const at::Tensor& t = tensor(a[3], "draft_probs");
+      need(t.dim() == 3 && t.scalar_type() == p.scalar_type() && t.size(0) == B && t.size(1) == K &&
+               t.size(2) == p.size(2) && step_of(t, 2) == 1,
+           "draft_probs must be [B, K, V] in target_probs' type, last dimension contiguous");
+      place.also(t);
+      d.draft_request_stride = step_of(t, 0);
+      d.draft_row_stride = step_of(t, 1);
+      q = t.data_ptr();
+    }
+    auto ints = [&](PyObject* o, const char* name) -> int32_t* {
+      if (!given(o)) return nullptr;
+      const at::Tensor& t = tensor(o, name);
+      vec(t, name, at::kInt, B);
+      place.also(t);
+      return t.data_ptr<int32_t>();
+    };
+    const int32_t *num = ints(a[4], "num_drafts"), *ctx = ints(a[5], "context_lens");
+    need(given(a[5]) || !given(a[8]), "next_lens needs context_lens");
+    at::Tensor out[3];
+    if (given(a[6])) {
+      out[0] = tensor(a[6], "tokens");
+      need(out[0].dim() == 2 && out[0].scalar_type() == at::kInt && out[0].is_contiguous() && out[0].size(0) == B &&
+               out[0].size(1) == K + 1,
+           "tokens must be a contiguous int32 [B, K + 1] tensor");
+      place.also(out[0]);
+    } else {
+      out[0] = at::empty({B, K + 1}, tok.options());
+    }
+    for (int i = 1; i < 3; ++i) {
+      if (i == 2 && !given(a[5])) break;
+      if (given(a[6 + i])) {
+        ints(a[6 + i], i == 1 ? "num_accepted" : "next_lens");
+        out[i] = tensor(a[6 + i], "");
+      } else {
+        out[i] = at::empty({B}, tok.options());
+      }
+    }
+    const qsa_status st =
+        qsa_verify_drafts(&d, tok.data_ptr<int32_t>(), num, p.data_ptr(), q, u.data_ptr<float>(), ctx,
+                          out[0].data_ptr<int32_t>(), out[1].data_ptr<int32_t>(),
+                          out[2].defined() ? out[2].data_ptr<int32_t>() : nullptr, place.stream());
+    PyObject* r = PyTuple_New(4);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, PyLong_FromLong(st));
+    for (int i = 0; i < 3; ++i) {
+      if (out[i].defined()) {
+        PyTuple_SET_ITEM(r, i + 1, wrap(out[i]));
+      } else {
+        Py_INCREF(Py_None);
+        PyTuple_SET_ITEM(r, i + 1, Py_None);
+      }
+    }
+    return r;
+  });
+}
+
 template <typename F>
 constexpr PyCFunction fast(F f) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -480,6 +712,8 @@ PyMethodDef methods[] = {
     {"store_paged_kv", fast(store_paged_kv), METH_FASTCALL, nullptr},
     {"store_index_keys", fast(store_index_keys), METH_FASTCALL, nullptr},
     {"paged_attention", fast(paged_attention), METH_FASTCALL, nullptr},
+    {"rotate_heads", fast(rotate_heads), METH_FASTCALL, nullptr},
+    {"verify_drafts", fast(verify_drafts), METH_FASTCALL, nullptr},
     {"drop_workspaces", fast(drop_workspaces), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -11,6 +11,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _abi
+from .rotary import Rotary
 
 
 class _Binding:
@@ -23,7 +24,8 @@ class _Binding:
         except ImportError as e:
             raise RuntimeError("_qsa_torch is not built for this torch: run "
                                "`python -c 'import __graft_entry__ as g; g.build()'`") from e
-        for n in ("build_page_maps", "store_paged_kv", "store_index_keys", "paged_attention", "drop_workspaces"):
+        for n in ("build_page_maps", "store_paged_kv", "store_index_keys", "paged_attention", "rotate_heads",
+                  "verify_drafts", "drop_workspaces"):
             setattr(self, n, getattr(mod, n))
         return getattr(mod, name)
 
@@ -271,7 +273,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                     max_new: int = 0, selected: Optional[torch.Tensor] = None, ratio: int = 1, local_tokens: int = 0,
                     form: int = _abi.ATTN_AUTO, out: Optional[torch.Tensor] = None,
                     lse: Optional[torch.Tensor] = None, return_lse: bool = False,
-                    workspace: Optional[torch.Tensor] = None, stream=None):
+                    workspace: Optional[torch.Tensor] = None, stream=None, window: int = 0, sink_tokens: int = 0):
     """Attention of the requests' new tokens over their paged cache
     (include/qsa.h, qsa_paged_attention): out [T, num_q_heads, head_dim], and
     with return_lse (or a given lse tensor) also lse fp32 [T, num_q_heads].
@@ -283,7 +285,10 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     1/sqrt(head_dim) unless given.  max_new: the host's bound on a request's new tokens (0:
     unknown), which only chooses the kernel form.  selected: int32 [T, k]
     columns of `ratio` tokens (select_topk's output): a row then sees these and
-    its last `local_tokens` tokens only.
+    its last `local_tokens` tokens only.  window > 0: a row sees the last `window`
+    tokens, its own among them, and the first `sink_tokens` ones only (pages
+    behind the window may be freed, their table entries hold anything); not
+    together with selected.
 
     Without a workspace, one is kept for each stream that calls (the 32 streams
     that called last); a call under
@@ -293,9 +298,11 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         with _on(stream):
             return paged_attention(q, k_cache, v_cache, block_table, query_start, seq_lens, scale=scale,
                                    max_new=max_new, selected=selected, ratio=ratio, local_tokens=local_tokens,
-                                   form=form, out=out, lse=lse, return_lse=return_lse, workspace=workspace)
+                                   form=form, out=out, lse=lse, return_lse=return_lse, workspace=workspace,
+                                   window=window, sink_tokens=sink_tokens)
     st, out, lse = _qsa_torch.paged_attention(q, k_cache, v_cache, block_table, query_start, seq_lens, scale, max_new,
-                                              selected, ratio, local_tokens, form, out, lse, return_lse, workspace)
+                                              selected, ratio, local_tokens, form, out, lse, return_lse, workspace,
+                                              window, sink_tokens)
     if st:
         _abi._check(st)
     return out if lse is None else (out, lse)
@@ -306,3 +313,92 @@ def drop_attention_workspaces() -> None:
     makes a new one).  device_status does so itself when it clears bit 3, a call
     that gave up on a wait: that may leave their counters uncleared."""
     _qsa_torch.drop_workspaces()
+
+
+# ---- between the projections and the cache, and after the logits -------------
+
+_NORMS = {None: _abi.NORM_NONE, "rms": _abi.NORM_RMS, "layer": _abi.NORM_LAYER}
+
+
+def rotate_heads(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, rotary: Rotary, *,
+                 norm: Optional[str] = None, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, q_bias: Optional[torch.Tensor] = None,
+                 k_bias: Optional[torch.Tensor] = None, eps: float = 1e-6, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, stream=None):
+    """(q, k) rotated by their positions, each head normalised first if `norm` is
+    "rms" or "layer" (include/qsa.h, qsa_rotate_heads); k None: (q, None).
+
+    q, k: bf16 or fp16 [T, heads, head_dim], any token and head strides (multiples
+    of 8 elements), head_dim a multiple of 8 up to 256; positions: int32 [T]
+    (build_page_maps' positions), negative ones mark padding rows, whose outputs
+    are not written; weights and biases: [head_dim], in q's type or fp32 (ones and
+    zeros unless given).  The outputs are new tensors unless given; q_out=q and
+    k_out=k rotate in place."""
+    if stream is not None:
+        with _on(stream):
+            return rotate_heads(q, k, positions, rotary, norm=norm, q_weight=q_weight, k_weight=k_weight, q_bias=q_bias,
+                                k_bias=k_bias, eps=eps, q_out=q_out, k_out=k_out)
+    _need(norm in _NORMS, "norm must be None, 'rms' or 'layer'")
+    st, q_out, k_out = _qsa_torch.rotate_heads(
+        q, k, positions, rotary.freqs, rotary.layout, rotary.offset, rotary.magnitude, _NORMS[norm], q_weight, k_weight,
+        q_bias, k_bias, eps, q_out, k_out, None, None, None, None)
+    if st:
+        _abi._check(st)
+    return q_out, k_out
+
+
+def rotate_store_kv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+                    k_cache: torch.Tensor, v_cache: torch.Tensor, rotary: Rotary, *, norm: Optional[str] = None,
+                    q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                    q_bias: Optional[torch.Tensor] = None, k_bias: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                    q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """rotate_heads and store_paged_kv in one pass (include/qsa.h,
+    qsa_rotate_store_kv): the rotated q is returned, the rotated keys and the
+    values v go to their cache slots.  slots int64 [T] and the caches as in
+    store_paged_kv; a row without a slot stores nothing, a row with a negative
+    position is padding altogether."""
+    if stream is not None:
+        with _on(stream):
+            return rotate_store_kv(q, k, v, positions, slots, k_cache, v_cache, rotary, norm=norm, q_weight=q_weight,
+                                   k_weight=k_weight, q_bias=q_bias, k_bias=k_bias, eps=eps, q_out=q_out)
+    _need(norm in _NORMS, "norm must be None, 'rms' or 'layer'")
+    _need(v is not None, "v must be a tensor")
+    st, q_out, _ = _qsa_torch.rotate_heads(
+        q, k, positions, rotary.freqs, rotary.layout, rotary.offset, rotary.magnitude, _NORMS[norm], q_weight, k_weight,
+        q_bias, k_bias, eps, q_out, None, v, slots, k_cache, v_cache)
+    if st:
+        _abi._check(st)
+    return q_out
+
+
+class Verified(NamedTuple):
+    """What verify_drafts writes."""
+    tokens: torch.Tensor                # int32 [B, K + 1]: accepted drafts, the next token, then -1
+    num_accepted: torch.Tensor          # int32 [B]
+    next_lens: Optional[torch.Tensor]   # int32 [B]: context_lens + 1 + num_accepted
+
+
+def verify_drafts(draft_tokens: torch.Tensor, target_probs: torch.Tensor, uniforms: torch.Tensor, *,
+                  draft_probs: Optional[torch.Tensor] = None, num_drafts: Optional[torch.Tensor] = None,
+                  context_lens: Optional[torch.Tensor] = None, out: Optional[Verified] = None, stream=None) -> Verified:
+    """Which drafted tokens the target accepts, and the token after them, from
+    given random numbers (include/qsa.h, qsa_verify_drafts).
+
+    draft_tokens: int32 [B, K] (K 0: the next token alone is drawn); target_probs:
+    fp32, bf16 or fp16 [B, K + 1, V], rows contiguous; uniforms: fp32 [B, K + 1] in
+    [0, 1): one a draft, the last for the next token; draft_probs: [B, K, V] in
+    the same type (None: certain drafts, accepted with the target's probability);
+    num_drafts: int32 [B] drafts a request brings (None: K).  With context_lens,
+    int32 [B] tokens in the cache before the step, next_lens are the ones that
+    count after it (the rejected drafts' slots are overwritten by later steps)."""
+    if stream is not None:
+        with _on(stream):
+            return verify_drafts(draft_tokens, target_probs, uniforms, draft_probs=draft_probs, num_drafts=num_drafts,
+                                 context_lens=context_lens, out=out)
+    given = (None, None, None) if out is None else out
+    _need(len(given) == 3, "out must be a Verified")
+    st, tokens, accepted, lens = _qsa_torch.verify_drafts(draft_tokens, target_probs, uniforms, draft_probs, num_drafts,
+                                                          context_lens, *given)
+    if st:
+        _abi._check(st)
+    return Verified(tokens, accepted, lens)
