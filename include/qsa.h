@@ -687,7 +687,7 @@ typedef struct qsa_head_rows {
  *   lo' = m (lo cos a - hi sin a),   hi' = m (hi cos a + lo sin a);
  * elements beside the rotated part stay n (without a norm: their bits).  All in
  * fp32, rounded to the rows' type once.  Rows with a negative position are
- * padding: neither read nor written.
+ * padding: their outputs are not written.
  *
  * freqs: device uint64 [R / 2], f_i / (2 pi) in units of 2^-64, modulo 2^64: the
  * angle of a position is exact modulo a turn but for that rounding.  positions:
@@ -742,9 +742,9 @@ typedef struct qsa_verify_desc {
  * the cache holds that count, for a step that brought one token and the drafts
  * (saturates at 2^31-1; both pointers or neither).
  *
- * Probabilities are clamped to [0, 1] (NaN: 0), those of a row add up to 8 at
- * most (else the next token is unspecified, in range).  Weights count in units
- * of 2^-60, so sums are exact and the result does not depend on their order.
+ * Probabilities are clamped to [0, 1] (NaN: 0), those of a row add up to 1024 at
+ * most (else the request's outputs are unspecified).  Weights count in units
+ * of 2^-45, so sums are exact and the result does not depend on their order.
  * u outside [0, 1) is taken as the nearest inside (NaN: 0).  No weight at all:
  * the next token is -1.  Rows past n (target) and n - 1 (draft) may hold
  * anything; so may draft_tokens past n.

@@ -7,17 +7,20 @@
 // from p_n: the smallest j whose cumulative weight exceeds u times the total.
 // Accepted so, the tokens are distributed as the target's own samples.
 //
-// The sums are integers: a probability counts in units of 2^-60 (exactly, from
-// 2^-36 up in fp32), so totals and cumulative sums do not depend on the order in
-// which the parts are added, and the comparison u * total < cumulative is exact
-// too.  A row's weights are summed once, by a cluster of CTAs that each take a
-// contiguous share and each warp a contiguous part of it; the totals cross the
-// cluster through shared memory, and the one warp whose part holds the drawn
-// point reads that part again.
+// Weights count in units of 2^-45 (exactly, from 2^-22 up in fp32), so totals and
+// cumulative sums do not depend on the order in which the parts are added, and the
+// comparison u * total < cumulative is exact too.  A row's weights are summed
+// once, by a cluster of CTAs that each take a contiguous share and each warp a
+// contiguous part of it; the totals cross the cluster through shared memory, and
+// the CTA whose share holds the drawn point reads the one part that does again, a
+// group of tokens a warp.
 //
 // What bounds it: the row of p (and of q) of each request, from HBM, once; for
 // few requests the chain of loads ahead of the row (the drafts, their
-// probabilities) and the cluster's exchange.
+// probabilities), the row, and the cluster's exchange; between the two the sums'
+// instructions.  Units comes to six a value: integer significands shifted into 64
+// bits took 54 (those instructions run at half rate or less), 27 us for 64 requests
+// x 131072 tokens, three exact fp32 accumulators nine, 20 us.
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -30,9 +33,9 @@
 namespace qsa {
 namespace {
 
-constexpr int kNT = 256;
+constexpr int kNT = 512;
 constexpr int kWarps = kNT / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;  // above 8: where the device takes such clusters
 constexpr uint32_t kAll = 0xffffffffu;
 
 template <typename T>
@@ -44,8 +47,78 @@ __device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 v) { retu
 template <>
 __device__ __forceinline__ float as_float<__half>(__half v) { return __half2float(v); }
 
-// A probability in units of 2^-60, clamped to [0, 1]; NaN counts as 0.
-__device__ __forceinline__ uint64_t units_of(float p) { return __float2ull_rn(__saturatef(p) * 0x1p60f); }
+// The units of a probability in [0, 1]: the significand times a power of two.
+// Below 2^-22, where that would be a fraction, the sum with 2^-22 rounds to whole
+// units (ties to even), which the difference of the bit patterns counts.
+__device__ __forceinline__ uint64_t units_of(float p) {
+  const uint32_t bits = __float_as_uint(p);
+  if (p < 0x1p-22f) return __float_as_uint(p + 0x1p-22f) - __float_as_uint(0x1p-22f);
+  return (uint64_t)((bits & 0x7FFFFFu) | 0x800000u) << ((bits >> 23) - 105);
+}
+
+using f2 = uint64_t;  // two fp32 values in a register pair
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 sub2(f2 a, f2 b, f2 minus) {  // minus: (-1, -1)
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(b), "l"(minus), "l"(a));
+  return r;
+}
+
+// A sum of values in [-1, 1], two a call, in units of 2^-45.  Added to 3 a value is
+// rounded to a multiple of 2^-22, which the bit pattern counts from that of 3; the
+// rest, found without error, added to 1.5 * 2^-22 likewise to one of 2^-45 (ties to
+// even).  Both counts stay within 22 bits and their sign, so kValues of them, and
+// the patterns they are counted from, add up in 32 bits.
+struct Units {
+  static constexpr int kValues = 128;
+  static constexpr float kFirst = 3.0f, kSecond = 0x1.8p-22f;
+  uint32_t high = 0, low = 0;
+  uint64_t sum = 0;
+  __device__ __forceinline__ void add(f2 v, f2 minus) {
+    const f2 first = pair(kFirst, kFirst);
+    const f2 t = add2(v, first);
+    const f2 r = sub2(v, sub2(t, first, minus), minus);
+    const f2 s = add2(r, pair(kSecond, kSecond));
+    uint32_t x, y;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(t));
+    high += x + y;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(s));
+    low += x + y;
+  }
+  // To whole units, after n values.
+  __device__ __forceinline__ void total(uint32_t n) {
+    const int32_t h = (int32_t)(high - n * __float_as_uint(kFirst)), l = (int32_t)(low - n * __float_as_uint(kSecond));
+    sum += (uint64_t)((int64_t)h * (1LL << 23) + l);
+    high = low = 0;
+  }
+};
+
+// Which of the kWarps sums in shared memory `want` falls into, counted from the
+// first: the lowest k with sums[0] + .. + sums[k] >= want (kWarps: none, `want`
+// is left less all of them).  By a whole warp; want less the sums before.
+__device__ __forceinline__ int find(const uint64_t* sums, uint64_t& want) {
+  const int lane = (int)threadIdx.x & 31;
+  const uint64_t mine = lane < kWarps ? sums[lane] : 0;
+  uint64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < kWarps; o <<= 1) {
+    const uint64_t v = __shfl_up_sync(kAll, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const uint32_t hit = __ballot_sync(kAll, lane < kWarps && incl >= want);
+  const int k = hit ? __ffs(hit) - 1 : kWarps;
+  want -= __shfl_sync(kAll, hit ? incl - mine : incl, hit ? k : kWarps - 1);
+  return k;
+}
 
 // The probability of a drafted token as a double, clamped the same way.
 template <typename T>
@@ -59,39 +132,30 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
   return v;
 }
 
-// kV consecutive probabilities, 16 bytes of them.
+// kV probabilities from 16 bytes of them, in [0, 1].
 template <typename T, int kV>
-__device__ __forceinline__ void load_vec(const T* p, float (&v)[kV]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack(const uint4& w, float (&v)[kV]) {
   const T* e = reinterpret_cast<const T*>(&w);
 #pragma unroll
-  for (int i = 0; i < kV; ++i) v[i] = as_float(e[i]);
+  for (int i = 0; i < kV; ++i) v[i] = __saturatef(as_float(e[i]));
 }
 
-// What a row's tokens weigh: max(p - q, 0), p where nothing was refused.
-template <typename T>
-struct Row {
-  const T* p;
-  const T* q;      // null: no draft distribution
-  int64_t certain; // the refused certain draft, -1 none
-
-  __device__ __forceinline__ uint64_t weight(float pv, float qv, int64_t j, uint64_t& full) const {
-    const uint64_t a = units_of(pv);
-    full = a;
-    if (q != nullptr) {
-      const uint64_t b = units_of(qv);
-      return a > b ? a - b : 0;
-    }
-    // a certain draft has all its distribution's weight: 2^60 units, never below p's
-    return j == certain ? 0 : a;
-  }
-};
+// The lane's kV probabilities of group g of a row, zeros past the vocabulary.
+template <typename T, int kV>
+__device__ __forceinline__ uint4 load_group(const T* row, int32_t g, int32_t vocab, bool vec) {
+  const int32_t j0 = (g * 32 + ((int)threadIdx.x & 31)) * kV;
+  if (vec && j0 + kV <= vocab) return *reinterpret_cast<const uint4*>(row + j0);
+  T e[kV];
+#pragma unroll
+  for (int i = 0; i < kV; ++i) e[i] = j0 + i < vocab ? row[j0 + i] : T(0.0f);
+  return *reinterpret_cast<const uint4*>(e);
+}
 
 template <typename T>
-__global__ void __launch_bounds__(kNT) verify_kernel(const VerifyParams p, int cluster) {
+__global__ void __launch_bounds__(kNT, 2) verify_kernel(const VerifyParams p, int cluster) {
   constexpr int kV = 16 / (int)sizeof(T);
-  __shared__ uint64_t cta_sum[kMaxCluster][2];  // of every CTA of the cluster: refused weights, p
-  __shared__ uint64_t part_sum[kWarps][2];
+  __shared__ uint64_t cta_sum[2][kMaxCluster];  // of every CTA of the cluster; a second try's apart
+  __shared__ uint64_t part_sum[kWarps], group_sum[2][kWarps];
   const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
   const int b = (int)blockIdx.x / cluster, rank = (int)blockIdx.x - b * cluster;
   ptx::grid_dep_wait();
@@ -103,6 +167,7 @@ __global__ void __launch_bounds__(kNT) verify_kernel(const VerifyParams p, int c
   const T* draft = p.draft ? static_cast<const T*>(p.draft) + (int64_t)b * p.draft_request : nullptr;
   const float* u = p.uniforms + (int64_t)b * (p.max_drafts + 1);
   const int32_t* tokens = p.tokens + (int64_t)b * p.max_drafts;
+  const float uf = u[p.max_drafts];
   const int32_t n = p.num_drafts ? min(max(p.num_drafts[b], 0), p.max_drafts) : p.max_drafts;
 
   // ---- accepted drafts, by every warp for itself
@@ -126,138 +191,160 @@ __global__ void __launch_bounds__(kNT) verify_kernel(const VerifyParams p, int c
     if (i0 + 32 >= n) break;
   }
 
-  Row<T> row;
-  row.p = target + (int64_t)a * p.target_row;
-  row.q = a < n && draft ? draft + (int64_t)a * p.draft_row : nullptr;
-  row.certain = a < n && !draft ? tokens[a] : -1;
+  // The row's weights: max(p - q, 0) of a refused draft's, or p but for the certain
+  // draft (all its distribution's weight: never below p's); p alone otherwise.
+  bool refused = a < n;
+  const T* row = target + (int64_t)a * p.target_row;
+  const T* less = refused && draft ? draft + (int64_t)a * p.draft_row : nullptr;
+  int32_t without = refused && !draft ? tokens[a] : -1;
 
-  // ---- this warp's part of the row: [v0, v1), whole groups of 32 * kV but for the row's end
+  // ---- the parts of the row: groups of 32 * kV tokens, of which a lane has kV
   constexpr int kGroup = 32 * kV;
-  const int64_t groups = (p.vocab + kGroup - 1) / kGroup;
-  const int64_t parts = (int64_t)cluster * kWarps, me = (int64_t)rank * kWarps + warp;
-  const int64_t each = groups / parts, more = groups - each * parts;
-  const int64_t g0 = me * each + min(me, more), g1 = g0 + each + (me < more ? 1 : 0);
-  const bool vec = ((reinterpret_cast<uintptr_t>(row.p) | reinterpret_cast<uintptr_t>(row.q)) & 15) == 0;
-  // A group's weights: lane l has elements l * kV .. l * kV + kV - 1 of it, in both ways of loading.
-  auto group_at = [&](int64_t g, float (&pv)[kV], float (&qv)[kV]) {
-    const int64_t j0 = g * kGroup + lane * kV;
-    if (vec && j0 + kV <= p.vocab) {
-      load_vec(row.p + j0, pv);
-      if (row.q) load_vec(row.q + j0, qv);
-    } else {
+  const int32_t groups = (p.vocab + kGroup - 1) / kGroup;
+  const int32_t parts = cluster * kWarps;
+  const int32_t each = groups / parts, more = groups - each * parts;
+  auto part_begin = [&](int32_t k) { return k * each + min(k, more); };
+  // 16-byte loads where every row allows them, else lane by lane.
+  const bool vec = p.vocab % kV == 0 && ((reinterpret_cast<uintptr_t>(row) | reinterpret_cast<uintptr_t>(less)) & 15) == 0;
+  uint64_t all = 0;
+  int attempt = 0;
+#pragma unroll 1
+  for (;; ++attempt) {
+    // max(p - q, 0) = p - min(p, q).  kAhead groups' loads are in flight.
+    constexpr int kAhead = 4;
+    uint32_t count = 0;  // values added since the last total
+    const f2 minus = pair(-1.0f, -1.0f);
+    Units units;
+    const int32_t g0 = part_begin(rank * kWarps + warp), g1 = part_begin(rank * kWarps + warp + 1);
+    const int32_t end = min(g1 * kGroup, p.vocab);
+    // The order of the values within a group is not looked at here: 32 neighbours a load.
+    auto batch = [&](const T* from, int32_t g, uint4 (&w)[kAhead]) {
 #pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        const bool in = j0 + i < p.vocab;
-        pv[i] = in ? as_float(row.p[j0 + i]) : 0.0f;
-        qv[i] = in && row.q ? as_float(row.q[j0 + i]) : 0.0f;
-      }
-    }
-  };
-  uint64_t left = 0, full = 0;
-  constexpr int kAhead = 4;
-  for (int64_t g = g0; g < g1; g += kAhead) {
-    float pv[kAhead][kV], qv[kAhead][kV];
+      for (int k = 0; k < kAhead; ++k) {
+        const int32_t j = (g + k) * kGroup;
+        w[k] = make_uint4(0, 0, 0, 0);
+        if (vec) {
+          if (j + lane * kV < end) w[k] = *reinterpret_cast<const uint4*>(from + j + lane * kV);
+        } else {
+          T* e = reinterpret_cast<T*>(&w[k]);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (g + k < g1) group_at(g + k, pv[k], qv[k]);
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (g + k < g1) {
-        const int64_t j0 = (g + k) * kGroup + lane * kV;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-          uint64_t f;
-          left += row.weight(pv[k][i], row.q ? qv[k][i] : 0.0f, j0 + i, f);
-          full += f;
+          for (int i = 0; i < kV; ++i)
+            if (j + i * 32 + lane < end) e[i] = from[j + i * 32 + lane];
         }
       }
-  }
-  left = warp_sum(left);
-  full = warp_sum(full);
-  if (lane == 0) {
-    part_sum[warp][0] = left;
-    part_sum[warp][1] = full;
-  }
-  __syncthreads();
-  // ---- totals to every CTA of the cluster
-  uint64_t mine[2] = {0, 0};
+    };
+#pragma unroll 1
+    for (int32_t g = g0; g < g1; g += kAhead) {
+      uint4 w[kAhead], v[kAhead];
+      batch(row, g, w);
+      if (less) batch(less, g, v);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    mine[0] += part_sum[w][0];
-    mine[1] += part_sum[w][1];
+      for (int k = 0; k < kAhead; ++k) {
+        if (g + k >= g1) break;
+        float pv[kV], qv[kV];
+        unpack<T, kV>(w[k], pv);
+#pragma unroll
+        for (int i = 0; i < kV; i += 2) units.add(pair(pv[i], pv[i + 1]), minus);
+        if (less) {
+          unpack<T, kV>(v[k], qv);
+#pragma unroll
+          for (int i = 0; i < kV; i += 2)
+            units.add(pair(fmaxf(-pv[i], -qv[i]), fmaxf(-pv[i + 1], -qv[i + 1])), minus);
+        }
+      }
+      count += min(kAhead, g1 - g) * (less ? 2 * kV : kV);
+      if (count > Units::kValues - 2 * kAhead * kV || g + kAhead >= g1) {
+        units.total(count);
+        count = 0;
+      }
+    }
+    uint64_t sum = warp_sum(units.sum);
+    if (without >= g0 * kGroup && without < end) sum -= units_of(__saturatef(as_float(row[without])));
+    if (lane == 0) part_sum[warp] = sum;
+    __syncthreads();
+    // ---- totals to every CTA of the cluster
+    if (attempt == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if ((int)threadIdx.x < cluster) {
+      uint64_t mine = 0;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) mine += part_sum[k];
+      uint32_t remote;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                   : "=r"(remote)
+                   : "r"(ptx::smem_u32(&cta_sum[attempt][rank])), "r"((int)threadIdx.x));
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote), "l"(mine) : "memory");
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    all = 0;
+    for (int c = 0; c < cluster; ++c) all += cta_sum[attempt][c];
+    if (all > 0 || !refused) break;
+    refused = false;  // nothing left of the refused row: p itself
+    less = nullptr;
+    without = -1;
   }
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if ((int)threadIdx.x < 2 * cluster) {
-    const int to = (int)threadIdx.x >> 1, which = (int)threadIdx.x & 1;
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                 : "=r"(remote)
-                 : "r"(ptx::smem_u32(&cta_sum[rank][which])), "r"(to));
-    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote), "l"(mine[which]) : "memory");
-  }
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 
-  // ---- the drawn point, and the warp whose part holds it
-  uint64_t total[2] = {0, 0};
-  for (int c = 0; c < cluster; ++c) {
-    total[0] += cta_sum[c][0];
-    total[1] += cta_sum[c][1];
-  }
-  const int which = total[0] > 0 ? 0 : 1;  // nothing left of a refused row: p itself
-  const uint64_t all = total[which];
-  const float uf = u[p.max_drafts];
-  // u in units of 2^-64, in [0, 1); point = floor(all * u), and a cumulative sum
-  // exceeds all * u exactly when it exceeds that
-  const uint64_t u64 = uf > 0.0f ? (uf < 1.0f ? (uint64_t)(uf * 0x1p64f) : ~0ull) : 0ull;
-  const uint64_t point = __umul64hi(all, u64);
-  uint64_t before = 0;
-  for (int c = 0; c < rank; ++c) before += cta_sum[c][which];
-  for (int w = 0; w < warp; ++w) before += part_sum[w][which];
-  int64_t next = -1;
-  if (all == 0) {
-    if (me != 0) return;  // no weight at all: no token
+  // ---- the drawn point: this CTA's, one of its parts', a token of one group
+  int32_t next = -1;
+  if (all == 0) {  // no weight at all: no token
+    if (rank != 0 || warp != 0) return;
   } else {
-    if (point < before || point - before >= part_sum[warp][which]) return;
-    const uint64_t want = point - before;  // the first j whose sum within this part exceeds it
-    uint64_t sum = 0;
-    for (int64_t g = g0; g < g1 && next < 0; ++g) {
+    // u in units of 2^-64, in [0, 1); point = floor(all * u), and a cumulative sum
+    // exceeds all * u exactly when it exceeds that
+    const uint64_t u64 = uf > 0.0f ? (uf < 1.0f ? (uint64_t)(uf * 0x1p64f) : ~0ull) : 0ull;
+    const uint64_t point = __umul64hi(all, u64);
+    uint64_t before = 0;
+    for (int c = 0; c < rank; ++c) before += cta_sum[attempt][c];
+    if (point < before || point - before >= cta_sum[attempt][rank]) return;
+    uint64_t want = point - before + 1;  // the first token with which the sum reaches this
+    const int part = min(find(part_sum, want), kWarps - 1);
+    const int32_t g1 = part_begin(rank * kWarps + part + 1);
+    int turn = 0;
+#pragma unroll 1
+    for (int32_t g = part_begin(rank * kWarps + part) + warp; next < 0; g += kWarps, turn ^= 1) {
+      if (g - warp >= g1) {  // (not reached: the part's sum is that of its groups)
+        if (warp != 0) return;
+        next = p.vocab - 1;
+        break;
+      }
+      const int32_t j0 = g * kGroup + lane * kV;
+      uint64_t wt[kV], own = 0;
       float pv[kV], qv[kV];
-      group_at(g, pv, qv);
-      const int64_t j0 = g * kGroup + lane * kV;
-      uint64_t w[kV], own = 0;
+      uint4 w = make_uint4(0, 0, 0, 0), v = w;
+      if (g < g1) {
+        w = load_group<T, kV>(row, g, p.vocab, vec);
+        if (less) v = load_group<T, kV>(less, g, p.vocab, vec);
+      }
+      unpack<T, kV>(w, pv);
+      unpack<T, kV>(v, qv);
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
-        uint64_t f;
-        const uint64_t l = row.weight(pv[i], row.q ? qv[i] : 0.0f, j0 + i, f);
-        w[i] = which == 0 ? l : f;
-        own += w[i];
+        wt[i] = pv[i] > qv[i] && j0 + i != without ? units_of(pv[i]) - units_of(qv[i]) : 0;
+        own += wt[i];
       }
       uint64_t incl = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t v = __shfl_up_sync(kAll, incl, o);
-        if (lane >= o) incl += v;
+        const uint64_t c = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += c;
       }
-      const uint32_t past = __ballot_sync(kAll, sum + incl > want);
-      if (past) {
-        const int src = __ffs(past) - 1;
-        uint64_t s = sum + incl - own;
-        int at = kV - 1;
+      if (lane == 31) group_sum[turn][warp] = incl;
+      __syncthreads();
+      const int at = find(group_sum[turn], want);
+      if (at == kWarps) continue;
+      if (at != warp) return;
+      uint64_t upto = incl - own;
+      int k = 0;  // the lane's tokens that do not reach it
 #pragma unroll
-        for (int i = kV - 1; i >= 0; --i) {  // from behind: the first that exceeds
-          uint64_t upto = s;
-#pragma unroll
-          for (int k = 0; k <= i; ++k) upto += w[k];
-          if (upto > want) at = i;
-        }
-        next = __shfl_sync(kAll, j0 + at, src);
+      for (int i = 0; i < kV; ++i) {
+        upto += wt[i];
+        k += upto < want ? 1 : 0;
       }
-      sum += __shfl_sync(kAll, incl, 31);
+      next = __shfl_sync(kAll, j0 + k, __ffs(__ballot_sync(kAll, incl >= want)) - 1);
     }
   }
   // ---- outputs
   int32_t* out = p.out_tokens + (int64_t)b * (p.max_drafts + 1);
-  for (int32_t i = lane; i <= p.max_drafts; i += 32) out[i] = i < a ? tokens[i] : (i == a ? (int32_t)next : -1);
+  for (int32_t i = lane; i <= p.max_drafts; i += 32) out[i] = i < a ? tokens[i] : (i == a ? next : -1);
   if (lane == 0) {
     p.num_accepted[b] = a;
     if (p.next_lens) {
@@ -272,10 +359,35 @@ cudaError_t launch_t(const VerifyParams& p, cudaStream_t stream) {
   DeviceInfo info;
   cudaError_t e = device_info(&info);
   if (e != cudaSuccess) return e;
-  // As many CTAs a request as fill the GPU twice over, while each has 2048 tokens or more.
+  // As many CTAs a request as the GPU holds at once (two an SM), while each warp has
+  // a group of tokens or more.
+  static std::atomic<uint64_t> known{0};  // devices asked
+  static std::atomic<int> at_once[64];    // clusters of 16 each of them holds
+  const uint64_t bit = info.device < 64 ? 1ull << info.device : 0;
+  if (!(known.load(std::memory_order_acquire) & bit)) {
+    int n = 0;
+    if (bit && cudaFuncSetAttribute(verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+      cudaLaunchConfig_t c = {};
+      c.gridDim = dim3(kMaxCluster, 1, 1);
+      c.blockDim = dim3(kNT, 1, 1);
+      cudaLaunchAttribute a[1];
+      a[0].id = cudaLaunchAttributeClusterDimension;
+      a[0].val.clusterDim.x = kMaxCluster;
+      a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
+      c.attrs = a;
+      c.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, verify_kernel<T>, &c) != cudaSuccess) n = 0;
+    }
+    cudaGetLastError();
+    if (bit) at_once[info.device].store(n, std::memory_order_relaxed);
+    known.fetch_or(bit, std::memory_order_release);
+  }
+  // Clusters of 16 only where all of them run at once (16 requests x 131072 tokens, one more
+  // than did: 12.0 us for 9.6).
+  const int most = bit && p.num_requests <= at_once[info.device].load(std::memory_order_relaxed) ? kMaxCluster : 8;
   int cluster = 1;
-  while (cluster < kMaxCluster && (int64_t)p.num_requests * cluster < 2 * info.num_sms &&
-         p.vocab >= (int64_t)cluster * 2 * 2048)
+  while (cluster < most && (int64_t)p.num_requests * cluster <= info.num_sms &&
+         (int64_t)p.vocab * (int)sizeof(T) >= (int64_t)cluster * 2 * kWarps * 512)
     cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.num_requests * cluster), 1, 1);

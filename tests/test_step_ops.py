@@ -541,11 +541,11 @@ def test_windowed_graph_replays_new_lengths(cuda):
 # ---------------------------------------------------------------------------
 
 def verified(tokens, target, uniforms, draft=None, num=None, context=None):
-    """In Python integers and float64; probabilities in units of 2^-60, as documented."""
+    """In Python integers and float64; probabilities in units of 2^-45, as documented."""
     B, K1, V = target.shape
     K = K1 - 1
     clean = lambda x: x.double().nan_to_num(0.0).clamp(0, 1).cpu().numpy()  # noqa: E731
-    units = lambda x: [int(v) for v in np.rint(x * 2.0 ** 60)]  # noqa: E731
+    units = lambda x: [int(v) for v in np.rint(x * 2.0 ** 45)]  # noqa: E731
     t, d = clean(target), None if draft is None else clean(draft)
     u = uniforms.double().nan_to_num(0.0).clamp(0, 1).cpu().numpy()
     out, acc = np.full((B, K1), -1), np.zeros(B, np.int64)
@@ -643,7 +643,7 @@ def test_verify_edges(cuda):
         "bad_token": ([-1, 3], [(4, 0.5), (4999, 0.5)], [(3, 1.0)], [(2, 1.0)]),
         "past_vocab": ([V, 3], [(0, 0.25), (4999, 0.75)], [(3, 1.0)], [(2, 1.0)]),
         "nan": ([1, 3], [(1, math.nan), (2, -1.0), (17, 0.5), (18, math.inf)], [(3, 1.0)], [(2, 1.0)]),
-        "tiny": ([5, 3], [(5, 2.0 ** -61), (40, 2.0 ** -60), (41, 2.0 ** -59)], [(3, 1.0)], [(2, 1.0)]),
+        "tiny": ([5, 3], [(5, 2.0 ** -46), (40, 2.0 ** -45), (41, 2.0 ** -22 - 2.0 ** -46), (42, 2.0 ** -22), (43, 3 * 2.0 ** -46)], [(3, 1.0)], [(2, 1.0)]),
     }
     us = [0.0, 1.0 - 2.0 ** -24, 1.0, 2.0, -1.0, math.nan, 0.5, 2.0 ** -40]
     for certain in (True, False):
@@ -664,6 +664,21 @@ def test_verify_edges(cuda):
             u[::2, :K] = 1.0
         got = torch_api.verify_drafts(tokens, target, u, draft_probs=draft)
         check_verified(got, verified(tokens, target, u, draft))
+
+
+@gpu
+@pytest.mark.parametrize("V", [700, 1000])
+def test_verify_weights_that_are_no_distribution(cuda, V):
+    """Rows of large weights, whose sum is far above 1: still exact."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    target = 1 - torch.rand((9, 2, V), generator=g, device="cuda") ** 9
+    target[0] = 1.0
+    draft = target[:, :1] * torch.rand((9, 1, V), generator=g, device="cuda")
+    tokens = torch.randint(0, V, (9, 1), dtype=torch.int32, device="cuda")
+    u = torch.rand((9, 2), generator=g, device="cuda")
+    for num in (None, _cu([0] * 9)):
+        got = torch_api.verify_drafts(tokens, target, u, draft_probs=draft, num_drafts=num)
+        check_verified(got, verified(tokens, target, u, draft, num))
 
 
 @gpu
