@@ -70,7 +70,8 @@ __device__ __forceinline__ int32_t item_units(const AttnParams& p, int32_t keys)
 // p - window < j or j < sinks.  The keys from the sinks' end to the window of the
 // item's first token are skipped: place `at` of an item's units holds key `at`
 // before sink_span and key at + skip from there on.  Both ends are multiples of
-// win_align (1: gathered rows, which lie anywhere; a tile of 128 keys otherwise).
+// win_align: 1 for gathered rows, which lie anywhere, the keys a copy brings (of
+// one page) for tiles, so that a tile may hold the sinks and the window's start.
 
 // First key of the window of the token at position pos.
 __device__ __forceinline__ int32_t window_from(const AttnParams& p, int32_t pos) {

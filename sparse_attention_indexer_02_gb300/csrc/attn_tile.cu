@@ -326,21 +326,21 @@ __global__ void __launch_bounds__(kNT, 1)
         // A box between the sinks and the window of every row: zeros are loaded in its place.
         auto unseen = [&](int32_t t) { return WIN && t >= p.sinks && t + box <= low0; };
         auto page_at = [&](int j) -> int32_t {  // the page of the lane's box of key tile j
-          const int32_t t = key_at<WIN>(p, j * kUnit, it.skip) + lane * box;
+          const int32_t t = key_at<WIN>(p, j * kUnit + lane * box, it.skip);
           return j < uz && lane * box < kUnit && t < it.keys && !unseen(t) ? table[t / p.page_tokens] : 0;
         };
         int32_t page = page_at(ua);
         for (int j = ua; j < uz && ok; ++j) {
-          const int32_t key0 = key_at<WIN>(p, j * kUnit, it.skip);
-          const int valid = min(kUnit, it.keys - key0);
+          const int32_t key = key_at<WIN>(p, j * kUnit + lane * box, it.skip);  // the lane's box's first
+          const int valid = min(kUnit, it.keys - (WIN ? it.skip : 0) - j * kUnit);
           const int nb = valid > 0 ? (valid + box - 1) / box : 0;
           // past the pool's end the copies write zeros
-          const int32_t pg = page == kNoPage || unseen(key0 + lane * box) ? p.num_pages
+          const int32_t pg = page == kNoPage || unseen(key) ? p.num_pages
                                                                           : min(max(page, 0), p.num_pages - 1);
           const uint32_t missing = __reduce_or_sync(
               0xffffffffu, page == kNoPage ? ((1u << (box >> 3)) - 1u) << (lane * (box >> 3)) : 0u);
           page = page_at(j + 1);
-          const int off = (key0 + lane * box) % p.page_tokens;
+          const int off = key % p.page_tokens;
           for (int kv = 0; kv < 2 && ok; ++kv, ++r) {
             const int st = r % kStages;
             ok = __all_sync(0xffffffffu, wait_phase(&empty[st], ((r / kStages) & 1u) ^ 1u, abort_flag, p.fault));
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kNT, 1)
         const ItemInfo& it = item_sh[items & 1u];
         if (!ok || it.a < 0) break;
         const int ua = it.a, uz = it.z, keys = it.keys, last_item = it.last;
-        const int skip = it.skip, low0 = WIN ? window_from(p, it.pos0) : 0;
+        const int skip = WIN ? it.skip : 0, low0 = WIN ? window_from(p, it.pos0) : 0;
         const int nst = it.n > tpt ? 2 : 1;
         ok = wwait(&full[stage], phase);
         if (!ok) break;
@@ -414,25 +414,26 @@ __global__ void __launch_bounds__(kNT, 1)
           if (!ok) break;
           advance();  // to the key tile of j + 1, if there is one
           const bool more = j + 1 < uz;
-          const int key0 = key_at<WIN>(p, j * kUnit, skip);
-          const int valid = max(0, min(kUnit, keys - key0));
+          const int valid = max(0, min(kUnit, keys - skip - j * kUnit));
           const int steps = (valid + 15) / 16;
           auto zero_rows = [&](int r0, int rows) {
-            uint8_t* v = smem + G::ring + vst * G::kTile;
-            for (int i = lane; i < rows * 8 * G::kHalves; i += 32)
-              *reinterpret_cast<uint4*>(v + (i / (rows * 8)) * (kRows * 128) + r0 * 128 + (i % (rows * 8)) * 16) =
-                  make_uint4(0, 0, 0, 0);
+            uint8_t* v = smem + G::ring + vst * G::kTile + r0 * 128;
+            for (int i = lane * 16; i < rows * 128; i += 512)
+#pragma unroll
+              for (int h = 0; h < G::kHalves; ++h)
+                *reinterpret_cast<uint4*>(v + h * (kRows * 128) + i) = make_uint4(0, 0, 0, 0);
           };
           bool zeroed = false;
           if (valid & 15) {  // the value rows between the last key and the product's end
             zero_rows(valid, steps * 16 - valid);
             zeroed = true;
           }
-          if (WIN && key0 + kUnit > p.sinks && key0 < low0) {
+          const int dead0 = p.sinks - j * kUnit, dead1 = low0 - skip - j * kUnit;  // windowed: rows no token sees
+          if (WIN && max(dead0, 0) < min(dead1, valid)) {
             // those between the sinks and the first row's window, but for the boxes loaded as
             // zeros: from the sinks' end to its box's, and from the window's box to its start
-            const int box = min(p.page_tokens, kUnit), end = min(low0 - key0, valid);
-            const int s0 = max(p.sinks - key0, 0), s1 = min((s0 + box - 1) / box * box, end);
+            const int box = min(p.page_tokens, kUnit), end = min(dead1, valid);
+            const int s0 = max(dead0, 0), s1 = min((s0 + box - 1) / box * box, end);
             const int w0 = max(end / box * box, s1);
             if (s0 < s1) zero_rows(s0, s1 - s0);
             if (w0 < end) zero_rows(w0, end - w0);
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(kNT, 1)
           const int tk = row / p.group;
           const int32_t lim = min(max(it.pos0 + st * tpt + tk + 1, 0), it.keys);  // keys [0, lim) are seen
           const int32_t low = WIN ? window_from(p, it.pos0 + st * tpt + tk) : 0;  // windowed: [low, lim) and the sinks
-          const int32_t skip = it.skip;
+          const int32_t skip = WIN ? it.skip : 0;
           // m in units of S.  Rows of no token (the tile's rows past its tokens, whose q is
           // whatever shared memory held) ask for no raise: it would move the warp's other rows.
           const bool live = tk < n && row < tpt * p.group;
@@ -548,10 +549,10 @@ __global__ void __launch_bounds__(kNT, 1)
             ptx::tmem_ld_done32(x[1]);
             ptx::tmem_ld32(t_s + 64, x[2]);  // on their way while the first half is worked on
             ptx::tmem_ld32(t_s + 96, x[3]);
-            const int key0 = key_at<WIN>(p, j * kUnit, skip);
-            const int seen = lim - key0;
-            const int from = WIN ? low - key0 : 0, sink = WIN ? p.sinks - key0 : 0;  // [sink, from) is masked
-            const bool edge = __any_sync(0xffffffffu, seen < kUnit || (WIN && from > 0 && sink < kUnit));
+            const int seen = lim - skip - j * kUnit;
+            // columns [sink, from) are masked
+            const int from = WIN ? low - skip - j * kUnit : 0, sink = WIN ? max(p.sinks - j * kUnit, 0) : 0;
+            const bool edge = __any_sync(0xffffffffu, seen < kUnit || (WIN && from > sink && sink < kUnit));
             float top[4];
             uint64_t sum[2];
             // The causal edge and the end of the keys: one block, out of the way of the loop,
@@ -857,8 +858,9 @@ cudaError_t launch_attn_tile(AttnParams p, const qsa_attn_desc& d, uint8_t* work
   p.tpi = 2 * tpt;
   p.min_shift = 1;
   p.item_cost = kItemCost;
-  p.win_align = kUnit;
-  p.sink_span = (p.sinks + kUnit - 1) / kUnit * kUnit;
+  // sinks and window both begin at a box of the copies (a multiple of its keys)
+  p.win_align = p.page_tokens < kUnit ? p.page_tokens : kUnit;
+  p.sink_span = (p.sinks + p.win_align - 1) / p.win_align * p.win_align;
   p.out32 = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.out_token_stride % 32 == 0 && p.out_head_stride % 32 == 0;
   const CUtensorMapDataType ty = f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap qm, km, vm;

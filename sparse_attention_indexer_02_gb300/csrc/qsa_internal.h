@@ -136,7 +136,8 @@ struct RotateParams {
   int64_t k_page_stride, k_token_stride, k_head_stride, v_page_stride, v_token_stride, v_head_stride;
   int64_t num_tokens, num_slots;
   int32_t page_tokens, head_dim, rot_dim, rot_offset, layout, norm, weight32;
-  int32_t per_warp, part_end[3];  // passes a warp takes; where q's, k's and v's of a token end
+  int32_t part_end[3];                // where q's, k's and v's passes of a token end
+  int32_t tokens;                     // tokens a CTA takes
   float eps, inv_dim, magnitude;
 };
 cudaError_t launch_rotate_bf16(const RotateParams& p, cudaStream_t stream);
