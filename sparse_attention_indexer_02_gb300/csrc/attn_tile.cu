@@ -407,6 +407,11 @@ __global__ void __launch_bounds__(kNT, 1)
         for (int st = 0; st < nst; ++st)
           issue_qk<D>(tmem + st * 128, q_lo + st * kTile16, k_lo + stage * kTile16, qk_hi, id_qk, &s_full[st],
                       &empty[stage], st == nst - 1);
+        // After the item's last scores q's place is free: the next item's q, and its first keys
+        // and values behind it, are on their way during the last softmax and product (1024 items
+        // of one key tile 58 -> 46 us, 8 x 1000 new tokens 102 -> 94, 8192 at 8192 396 -> 376;
+        // items of 33 tiles as before, to 2 %).
+        if (ua + 1 >= uz) ptx::mma_commit_elect(&q_bar[1]);
         advance();
         for (int j = ua; j < uz; ++j) {
           const uint32_t vst = stage;
@@ -469,14 +474,13 @@ __global__ void __launch_bounds__(kNT, 1)
               }
               issue_qk<D>(tmem + st * 128, q_lo + st * kTile16, k_lo + stage * kTile16, qk_hi, id_qk, &s_full[st],
                           &empty[stage], last);
+              if (last && j + 2 >= uz) ptx::mma_commit_elect(&q_bar[1]);
             }
           }
           if (!ok) break;
           if (more) advance();
         }
-        if (!ok) break;
-        ptx::mma_commit_elect(&q_bar[1]);
-        if (last_item) break;
+        if (!ok || last_item) break;
       }
       if (!ok) {
         ptx::mma_commit_elect(done);
