@@ -6,6 +6,18 @@ attention to the selected columns, all on the device.
     res = step(pool, block_table, context_lens, new_lens, free_pages, q=q, k=k, v=v, index_q=iq,
                index_keys=ik, index_weights=iw, top_k=2048, local_tokens=64, max_context=131072)
 
+A model's windowed layers share the step's page maps, and drafted tokens are
+verified after its last layer:
+
+    win = windowed(other_pool, block_table, res.maps, q=q, k=k, v=v, window=4096, sink_tokens=4,
+                   rotation=HeadRotation(rotary, norm="rms", q_weight=wq, k_weight=wk))
+    ver = torch_api.verify_drafts(drafts, target_probs, uniforms, draft_probs=dp, context_lens=context_lens)
+    context_lens = ver.next_lens
+
+(The pages of table entries past the next lengths hold refused tokens only; the
+caller may return them to its free list, or leave them: the next maps overwrite
+the entries.)
+
 Every call goes to the current stream, nothing waits for the device, and the
 shapes depend on host values only, so a step can be captured in a CUDA graph.
 """
@@ -41,6 +53,36 @@ class PagedPool:
             self.index_args = dict(page_cols=self.page_cols)
 
 
+class HeadRotation(NamedTuple):
+    """What a layer does to its queries and keys before they are stored: rotary
+    positions, after a norm of every head ("rms" or "layer") if there is one
+    (torch_api.rotate_store_kv)."""
+    rotary: torch_api.Rotary
+    norm: Optional[str] = None
+    q_weight: Optional[torch.Tensor] = None
+    k_weight: Optional[torch.Tensor] = None
+    q_bias: Optional[torch.Tensor] = None
+    k_bias: Optional[torch.Tensor] = None
+    eps: float = 1e-6
+
+
+def _store(pool: PagedPool, maps: torch_api.PageMaps, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+           rotation: Optional[HeadRotation]) -> torch.Tensor:
+    """The new tokens' keys and values into the pool; the queries attention takes."""
+    if rotation is None:
+        torch_api.store_paged_kv(k, v, maps.slots, pool.k_cache, pool.v_cache)
+        return q
+    rotary, *norm = rotation
+    names = HeadRotation._fields[1:]
+    return torch_api.rotate_store_kv(q, k, v, maps.positions, maps.slots, pool.k_cache, pool.v_cache, rotary,
+                                     **dict(zip(names, norm)))
+
+
+class WindowResult(NamedTuple):
+    out: torch.Tensor          # [T, num_q_heads, head_dim]
+    lse: torch.Tensor          # fp32 [T, num_q_heads]
+
+
 class StepResult(NamedTuple):
     out: torch.Tensor          # [T, num_q_heads, head_dim]
     lse: torch.Tensor          # fp32 [T, num_q_heads]
@@ -61,7 +103,8 @@ class StepResult(NamedTuple):
 def step(pool: PagedPool, block_table: torch.Tensor, context_lens: torch.Tensor, new_lens: torch.Tensor,
          free_pages: torch.Tensor, *, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, index_q: torch.Tensor,
          index_keys: torch.Tensor, index_weights: torch.Tensor, top_k: int, max_context: int, local_tokens: int = 0,
-         scale: Optional[float] = None) -> StepResult:
+         scale: Optional[float] = None, rotation: Optional[HeadRotation] = None,
+         index_rotary: Optional[torch_api.Rotary] = None) -> StepResult:
     """The step for B requests of T / B new tokens each (decode rows, rows to
     verify, or prompt chunks of one length; new_lens holds that count).
 
@@ -70,7 +113,10 @@ def step(pool: PagedPool, block_table: torch.Tensor, context_lens: torch.Tensor,
     key of the column a token completes; other rows are ignored) and
     index_weights [T, index heads] are request-major.  max_context bounds the
     requests' tokens.  A token attends to the top_k complete columns its index
-    scores select and to its last local_tokens tokens.
+    scores select and to its last local_tokens tokens.  With rotation, q and k are
+    normalised and rotated on their way (q and k as they come from the
+    projections); index_rotary rotates index_q (index_keys come rotated: a
+    column's position is the model's choice).
 
     Nothing of the device is read, so neither a new_lens that holds other counts
     nor a free list with too few pages raises: StepResult.valid() tells.
@@ -87,7 +133,9 @@ def step(pool: PagedPool, block_table: torch.Tensor, context_lens: torch.Tensor,
     maps = torch_api.build_page_maps(context_lens, new_lens, free_pages, block_table, page_tokens=pool.page_tokens,
                                      max_tokens=T, ratio=pool.ratio)
     scored_table = block_table.contiguous()
-    torch_api.store_paged_kv(k, v, maps.slots, pool.k_cache, pool.v_cache)
+    q = _store(pool, maps, q, k, v, rotation)
+    if index_rotary is not None:
+        index_q, _ = torch_api.rotate_heads(index_q, None, maps.positions, index_rotary)
     torch_api.store_index_keys(index_keys, maps.column_slots, pool.index, **pool.index_args)
     cols = max(1, max_context // pool.ratio)
     logits = torch_api.paged_mqa_logits(index_q, index_weights, pool.index, scored_table, maps.visible_cols,
@@ -97,3 +145,17 @@ def step(pool: PagedPool, block_table: torch.Tensor, context_lens: torch.Tensor,
                                          scale=scale, max_new=T // B, selected=selected, ratio=pool.ratio,
                                          local_tokens=local_tokens, return_lse=True)
     return StepResult(out, lse, selected, maps)
+
+
+def windowed(pool: PagedPool, block_table: torch.Tensor, maps: torch_api.PageMaps, *, q: torch.Tensor, k: torch.Tensor,
+             v: torch.Tensor, window: int, sink_tokens: int = 0, max_new: int = 0,
+             rotation: Optional[HeadRotation] = None, scale: Optional[float] = None) -> WindowResult:
+    """A windowed layer of a step whose page maps are built (step, or
+    torch_api.build_page_maps): the tokens' keys and values are stored in `pool`,
+    rotated first if asked, and every token attends to its last `window` tokens,
+    itself among them, and to the first sink_tokens ones.  Any number of tokens a
+    request; max_new as in torch_api.paged_attention."""
+    q = _store(pool, maps, q, k, v, rotation)
+    return WindowResult(*torch_api.paged_attention(q, pool.k_cache, pool.v_cache, block_table, maps.query_start,
+                                                   maps.seq_lens, scale=scale, max_new=max_new, window=window,
+                                                   sink_tokens=sink_tokens, return_lse=True))

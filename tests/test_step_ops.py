@@ -740,3 +740,114 @@ def test_step_operators_captured_and_on_another_stream(cuda):
             for a, b in zip(kept, got):
                 assert torch.equal(a, b)
             assert torch.equal(cache, pr.kc)
+
+
+# ---------------------------------------------------------------------------
+# runs of them together
+# ---------------------------------------------------------------------------
+
+def _plain_window(q, k, v, first, window, sinks):
+    """fp64 attention of the last tokens, at positions first.., to keys 0.. ."""
+    n, H, D = q.shape
+    s = k.shape[0]
+    pos = torch.arange(first, first + n, device="cuda")
+    j = torch.arange(s, device="cuda")
+    see = (j[None] <= pos[:, None]) & ((j[None] > pos[:, None] - window) | (j[None] < sinks))
+    kd, vd = (x.double().repeat_interleave(H // x.shape[1], 1) for x in (k, v))
+    x = torch.einsum("thd,shd->hts", q.double(), kd) * D ** -0.5
+    p = x.masked_fill(~see, -math.inf).softmax(-1)
+    return torch.einsum("hts,shd->thd", p, vd), torch.einsum("hts,shd->thd", p, vd.abs())
+
+
+@gpu
+@pytest.mark.parametrize("norm,layout", [("rms", "half"), (None, "pairs")])
+def test_speculative_rounds(cuda, norm, layout):
+    """Prompts, then rounds of four rows: maps, rotated stores, windowed attention and
+    verification, each round's lengths from the last one's on the device.  Refused
+    tokens are overwritten; attention is that of the accepted history alone."""
+    from sparse_attention_indexer_02_gb300 import serving
+
+    B, K, H, hkv, D, pt, window, sinks, V = 3, 3, 8, 2, 128, 16, 40, 5, 500
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    pool = serving.PagedPool(num_pages=120, page_tokens=pt, num_kv_heads=hkv, head_dim=D, ratio=4)
+    how = serving.HeadRotation(torch_api.Rotary(D, layout=layout), norm=norm,
+                               q_weight=1 + 0.1 * rnd(D) if norm else None, k_weight=1 + 0.1 * rnd(D) if norm else None)
+    table = torch.full((B, 20), -1, dtype=torch.int32, device="cuda")
+    pages = torch.randperm(120, generator=g, device="cuda").to(torch.int32)
+    ctx, new = _cu([0, 0, 0]), _cu([70, 3, 41])
+    hist, taken = [(torch.empty((0, hkv, D), device="cuda").bfloat16(),) * 2 for _ in range(B)], 0
+    for turn in range(7):
+        T = int(new.sum())
+        q, k, v = rnd(T, H, D), rnd(T, hkv, D), rnd(T, hkv, D)
+        maps = torch_api.build_page_maps(ctx, new, pages[taken:], table, page_tokens=pt, max_tokens=T)
+        taken += int(maps.pages_used)
+        res = serving.windowed(pool, table, maps, q=q, k=k, v=v, window=window, sink_tokens=sinks,
+                               max_new=int(new.max()), rotation=how)
+        kw = {n: getattr(how, n) for n in ("norm", "q_weight", "k_weight", "eps")}
+        qr, kr = torch_api.rotate_heads(q, k, maps.positions, how.rotary, **kw)
+        start = maps.query_start.tolist()
+        for b in range(B):
+            rows = slice(start[b], start[b + 1])
+            ks, vs = torch.cat([hist[b][0], kr[rows]]), torch.cat([hist[b][1], v[rows]])
+            want, mag = _plain_window(qr[rows], ks, vs, len(hist[b][0]), window, sinks)
+            # the rounded output and probabilities, half a step each; scores of about 30 in fp32
+            assert ((res.out[rows].double() - want).abs() <= 2.0 ** -8 * (want.abs() + mag) + 1e-4 * mag + 1e-6).all()
+        if turn == 0:      # the prompts count as they are
+            keep = new.tolist()
+            ctx = maps.seq_lens
+        else:
+            tokens, target, u, draft = _drafted(B, K, V, torch.float32, turn)
+            ver = torch_api.verify_drafts(tokens, target, u, draft_probs=draft, context_lens=ctx)
+            check_verified(ver, verified(tokens, target, u, draft, None, ctx))
+            keep = [1 + a for a in ver.num_accepted.tolist()]
+            ctx = ver.next_lens
+        hist = [(torch.cat([hist[b][0], kr[start[b]:start[b] + keep[b]]]),
+                 torch.cat([hist[b][1], v[start[b]:start[b] + keep[b]]])) for b in range(B)]
+        assert ctx.tolist() == [len(h[0]) for h in hist]
+        new = _cu([K + 1] * B)
+
+
+@gpu
+def test_serving_step_with_rotation(cuda):
+    """The step with a rotation is the step of the rotated queries and keys."""
+    from sparse_attention_indexer_02_gb300 import serving
+
+    B, n, H, hkv, D = 2, 40, 8, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(6)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    T = B * n
+    q, k, v, iq, ik = rnd(T, H, D), rnd(T, hkv, D), rnd(T, hkv, D), rnd(T, 4, 128), rnd(T, 128)
+    iw = torch.rand((T, 4), generator=g, device="cuda")
+    how = serving.HeadRotation(torch_api.Rotary(64, offset=64, layout="pairs"), "layer", rnd(D), rnd(D), rnd(D), rnd(D))
+    irot = torch_api.Rotary(64)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda").repeat(B)
+    qr, kr = torch_api.rotate_heads(q, k, pos, how.rotary, norm="layer", q_weight=how.q_weight, k_weight=how.k_weight,
+                                    q_bias=how.q_bias, k_bias=how.k_bias, eps=how.eps)
+    iqr = torch_api.rotate_heads(iq, None, pos, irot)[0]
+    got = []
+    for args, kw in (((qr, kr, iqr), {}), ((q, k, iq), dict(rotation=how, index_rotary=irot))):
+        pool = serving.PagedPool(num_pages=8, page_tokens=16, num_kv_heads=hkv, head_dim=D, ratio=4)
+        table = torch.full((B, 4), -1, dtype=torch.int32, device="cuda")
+        res = serving.step(pool, table, _cu([0, 0]), _cu([n, n]), _cu([5, 2, 7, 0, 3, 1, 6, 4]), q=args[0], k=args[1],
+                           v=v, index_q=args[2], index_keys=ik, index_weights=iw, top_k=5, local_tokens=8, max_context=64,
+                           **kw)
+        got.append((res.out, res.lse, res.selected, pool.k_cache, pool.v_cache))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+@gpu
+def test_rotations_on_two_streams_at_once(cuda):
+    """Calls that share their inputs and run beside one another."""
+    q = torch.randn((3000, 16, 128), device="cuda").to(torch.bfloat16)
+    pos = torch.arange(3000, dtype=torch.int32, device="cuda")
+    rots = [rotary.Rotary(128), rotary.Rotary(24, layout="half"), rotary.Rotary(64, layout="pairs", offset=64)]
+    want = [torch_api.rotate_heads(q, None, pos, r, norm="rms")[0] for r in rots]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in rots]
+    for _ in range(5):
+        got = [torch_api.rotate_heads(q, None, pos, r, norm="rms", stream=s)[0] for r, s in zip(rots, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
