@@ -851,3 +851,106 @@ def test_rotations_on_two_streams_at_once(cuda):
         torch.cuda.synchronize()
         for a, b in zip(want, got):
             assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------------------
+# places of tensors
+# ---------------------------------------------------------------------------
+
+def test_step_tensors_of_another_device_are_refused(lib):
+    """Tensors that say they are on device 1 (fake ones, without memory)."""
+    fake = pytest.importorskip("torch._subclasses.fake_tensor")
+    with fake.FakeTensorMode():
+        z = lambda dtype, *s: torch.empty(s, dtype=dtype, device="cuda:1")  # noqa: E731
+        b16, i32 = torch.bfloat16, torch.int32
+        q, k, pos, slots, kc = z(b16, 3, 8, 128), z(b16, 3, 2, 128), z(i32, 3), z(torch.int64, 3), z(b16, 4, 16, 2, 128)
+        tok, p, u, freqs = z(i32, 2, 3), z(torch.float32, 2, 4, 50), z(torch.float32, 2, 4), z(torch.int64, 64)
+    rot = rotary.Rotary(128, device="cpu")
+    rot.freqs = freqs
+    if torch.cuda.is_available():
+        assert torch.cuda.current_device() != 1
+    for call in (lambda: torch_api.rotate_heads(q, k, pos, rot),
+                 lambda: torch_api.rotate_store_kv(q, k, k, pos, slots, kc, kc, rot),
+                 lambda: torch_api.verify_drafts(tok, p, u)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
+
+
+@gpu
+def test_step_tensors_on_two_devices_are_refused(cuda):
+    q = torch.zeros((3, 8, 128), dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros(3, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="different devices"):
+        torch_api.rotate_heads(q, None, pos, rotary.Rotary(128, device="cpu"))
+    with pytest.raises(ValueError, match="different devices"):
+        torch_api.rotate_heads(q, q.cpu(), pos, rotary.Rotary(128))
+    tok, p, u = _cu([[1, 2]]), torch.rand((1, 3, 50), device="cuda"), torch.rand((1, 3), device="cuda")
+    for kw in (dict(draft_probs=p[:, :2].cpu()), dict(num_drafts=torch.ones(1, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="different devices"):
+            torch_api.verify_drafts(tok, p, u, **kw)
+
+
+@gpu
+def test_rows_and_slots_past_32_bits(cuda):
+    """Rows of q and k 3 GB apart, cache pages 5 GiB apart, probabilities 8 GB apart."""
+    T, D = 3, 128
+    step = 3 << 29                                  # elements of 2 bytes
+    far = torch.empty(2 * step + 4 * D, dtype=torch.bfloat16, device="cuda")
+    x = torch.as_strided(far, (T, 2, D), (step, D, 1))
+    x.copy_(torch.randn((T, 2, D), device="cuda"))
+    q, k, v = x[:, :1], x[:, 1:], x[:, 1:]
+    rot, pos = rotary.Rotary(D), _cu([7, 8, 9])
+    want = torch_api.rotate_heads(q.contiguous(), k.contiguous(), pos, rot, norm="rms")
+    page = 5 << 29
+    buf = torch.empty(2 * page + 4 * D, dtype=torch.bfloat16, device="cuda")
+    kc = torch.as_strided(buf, (3, 1, 1, D), (page, D, D, 1))
+    vc = torch.empty((3, 1, 1, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.as_strided(far, (T, 1, D), (step, D, 1), 2 * D)
+    torch_api.rotate_store_kv(q, k, v, pos, torch.tensor([2, 0, 1], device="cuda"), kc, vc, rot, norm="rms", q_out=out)
+    at = [1, 2, 0]                                  # the token that went to each page
+    assert torch.equal(out, want[0]) and torch.equal(kc[:, 0], want[1][at]) and torch.equal(vc[:, 0], v[at])
+    del buf, kc, far, x, q, k, v, out
+    V, gap = 1000, 2 << 30                          # fp32: 8 GB from row to row
+    tokens, target, u, draft = _drafted(1, 2, V, torch.float32, 9)
+    wide = torch.empty(2 * gap + V, device="cuda")
+    rows = torch.as_strided(wide, (1, 3, V), (3 * gap, gap, 1))
+    rows.copy_(target)
+    for uu in (u, torch.zeros_like(u)):
+        check_verified(torch_api.verify_drafts(tokens, rows, uu, draft_probs=draft), verified(tokens, target, uu, draft))
+
+
+@gpu
+def test_first_calls_under_capture(cuda):
+    """A process whose first calls of the operators are captured, and then replayed."""
+    import subprocess
+    import sys
+
+    code = """
+import torch
+from sparse_attention_indexer_02_gb300 import torch_api
+q = torch.randn((5, 8, 128), device="cuda").to(torch.bfloat16)
+k = q[:, :2].contiguous()
+kc = torch.zeros((2, 4, 16, 2, 128), dtype=torch.bfloat16, device="cuda")
+i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+rot, pos, slots = torch_api.Rotary(128), torch.arange(5, dtype=torch.int32, device="cuda"), torch.arange(5, device="cuda")
+table, start, seq = i32(0, 1, 2, 3).view(1, 4), i32(0, 5), i32(5)
+tok, p, u = i32(3, 4).view(1, 2), torch.softmax(torch.randn((1, 3, 70000), device="cuda"), 2), torch.rand((1, 3), device="cuda")
+ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+def run():
+    r = torch_api.rotate_store_kv(q, k, k, pos, slots, kc[0], kc[1], rot, norm="rms")
+    o = torch_api.paged_attention(r, kc[0], kc[1], table, start, seq, window=3, sink_tokens=1, workspace=ws)
+    return r, o, torch_api.verify_drafts(tok, p, u).tokens
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = run()
+g.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in got]
+for a, b in zip(got, run()):
+    assert torch.equal(a, b)
+print("same")
+"""
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                         cwd=qbuild.PKG + "/..")
+    assert res.returncode == 0 and "same" in res.stdout, res.stderr[-2000:]
