@@ -164,7 +164,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if lib_ok and binding_ok:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    srcs = [] if lib_ok else _sources()
+    srcs = [] if lib_ok else _sources()[::-1]  # the scorer's units (umma_*) take longest: first
     with cf.ThreadPoolExecutor(max_workers=max(1, min(16, os.cpu_count() or 8))) as ex:
         binding = ex.submit(_compile_binding) if not binding_ok else None
         done = list(ex.map(_compile, srcs))

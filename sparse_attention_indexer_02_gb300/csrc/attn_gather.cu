@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
   Item it;
   if (SEL) it = selected_item(p, s.u0, sel_units, 0);
   else it = Walker<WIN>(p, at, s.u0).it;
-  if (!first_part(p, s, it, next)) return;
+  if (!first_part<WIN>(p, s, it, next)) return;
   // Registers: 512 threads of 128 at launch, 256 * 72 + 256 * 176 are less; or
   // 384 of 168, of which 128 * 88 + 256 * 208 is the same sum.
   if (warp >= kConsumers) {
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
     uint32_t n = 0;                      // slices filled, of any of its consumers
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
-      const Part part(p, s, it);
+      const Part<WIN> part(p, s, it);
       const int ua = part.a, uz = part.z;
       const int kvh = p.splits == 1 ? it.hv : it.hv / p.splits;
       const int sub0 = (it.hv - kvh * p.splits) * p.sub;
@@ -303,8 +303,8 @@ __global__ void __launch_bounds__(Conf<MT>::kNT, 1) attn_gather_kernel(const Att
         o->n = it.n;
         o->pos0 = it.pos0;
         o->keys = it.keys;
-        o->c0 = first_cta(s, it);
-        o->c1 = last_cta(p, s, it);
+        o->c0 = first_cta<WIN>(p, s, it);
+        o->c1 = last_cta<WIN>(p, s, it);
         o->last = it.s1 >= s.u1;
         o->skip = it.skip;
         ptx::mbar_arrive(&q_full[k & 1]);
@@ -745,6 +745,7 @@ cudaError_t launch_attn_gather(AttnParams p, const qsa_attn_desc& d, uint8_t* wo
   p.tpi = p.num_selected > 0 ? 1 : 16 * mt / p.sub;
   p.min_shift = 0;
   p.item_cost = kItemCost;
+  p.whole_units = 5;
   p.win_align = 1;
   p.sink_span = p.sinks;
   p.ratio_shift = -1;

@@ -288,13 +288,13 @@ __global__ void __launch_bounds__(kNT, 1)
       bool ok = true;
       Walker<WIN> w(p, at, s.u0);
       const Item& it = w.it;
-      const bool any = first_part(p, s, w.it, [&](Item&) { w.next(); });
+      const bool any = first_part<WIN>(p, s, w.it, [&](Item&) { w.next(); });
       if (!any && lane == 0) {
         item_sh[0].a = -1;
         ptx::mbar_arrive(&q_bar[0]);
       }
       if (any) for (;;) {
-        const Part part(p, s, it);
+        const Part<WIN> part(p, s, it);
         const int ua = part.a, uz = part.z;
         const int nst = it.n > tpt ? 2 : 1;
         if (items > 0) ok = __all_sync(0xffffffffu, wait_phase(&q_bar[1], (items - 1) & 1u, abort_flag, p.fault));
@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(kNT, 1)
           o.pos0 = it.pos0;
           o.keys = it.keys;
           o.head0 = it.hv * p.group;
-          o.c0 = first_cta(s, it);
-          o.c1 = last_cta(p, s, it);
+          o.c0 = first_cta<WIN>(p, s, it);
+          o.c1 = last_cta<WIN>(p, s, it);
           o.last = it.s1 >= s.u1;
           o.skip = it.skip;
         }
@@ -862,6 +862,7 @@ cudaError_t launch_attn_tile(AttnParams p, const qsa_attn_desc& d, uint8_t* work
   p.tpi = 2 * tpt;
   p.min_shift = 1;
   p.item_cost = kItemCost;
+  p.whole_units = 0;
   // sinks and window both begin at a box of the copies (a multiple of its keys)
   p.win_align = p.page_tokens < kUnit ? p.page_tokens : kUnit;
   p.sink_span = (p.sinks + p.win_align - 1) / p.win_align * p.win_align;

@@ -177,6 +177,7 @@ struct AttnParams {
   int32_t min_shift;          // a CTA takes at least 2^min_shift units (fewer CTAs take part then)
   int32_t num_selected, ratio, ratio_shift, local_tokens;  // ratio_shift: log2, or -1
   int32_t window, sinks;      // windowed calls: a row's last tokens and the first ones; 0 else
+  int32_t whole_units;        // windowed calls: items of up to so many units of keys may stay undivided
   int32_t sink_span, win_align;  // sinks rounded up to win_align: places before the skipped keys
   int32_t near_rows;          // keys and values: equal strides, offsets below 2^36 bytes
   float scale_log2;           // scale * log2(e)

@@ -439,10 +439,8 @@ WINDOW_LENS = {
 def test_windowed_attention(cuda, form, lens, window, sinks, hkv, group, D, pt, dt):
     pr = Problem(WINDOW_LENS[lens], hkv, group, D, pt, dt, seed=len(lens) * 100 + group)
     windowed(pr, window, min(sinks, 2100), form)
-    if sinks > 2100:    # every token is a sink: full attention
-        a = pr.run(form=form)
-        b = pr.run(form=form, window=window, sink_tokens=sinks)
-        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    if sinks > 2100:    # every token is a sink: full attention (short items may be divided otherwise)
+        pr.check(*pr.run(form=form, window=window, sink_tokens=sinks))
 
 
 @gpu
