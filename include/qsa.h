@@ -611,7 +611,8 @@ qsa_status qsa_paged_attention(const qsa_attn_desc* desc, const void* q, const v
  * call sees may hold anything, so pages behind the window can be freed; cache
  * contents no row sees are never used, whatever they hold.  Time and bytes
  * follow the window, not seq_lens.  form and workspace as there
- * (qsa_paged_attention_workspace, qsa_plan_attention).
+ * (qsa_paged_attention_workspace, qsa_plan_attention), but that up to 32 query
+ * rows a key/value head are gathered when window + sink_tokens is at most 512.
  */
 qsa_status qsa_paged_attention_window(const qsa_attn_desc* desc, int32_t window, int32_t sink_tokens, const void* q,
                                       const void* k_cache, const void* v_cache, const int32_t* block_table,

@@ -190,6 +190,7 @@ constexpr int kGatherRows = 32;  // rows of the gathered form's largest tile
 // 21.8 / 25.7), at 20, where it needs a second row tile, it does not (90 / 92,
 // 60 / 59, 13.2 / 12.0; 32 rows: 91 / 93, 63 / 60, 14.2 / 12.4, 35.0 / 29.0).
 constexpr int kTileAbove = 16;
+constexpr int kGatherWindow = 512;  // windowed calls: keys up to which kGatherRows rows are gathered
 size_t attn_gather_workspace(int head_dim);
 size_t attn_tile_workspace(int head_dim);
 bool attn_tile_supports(const qsa_attn_desc& d, const char** why);

@@ -160,11 +160,11 @@ PyObject* guarded(F&& f) noexcept {
 }
 
 // A contiguous tensor of `sizes` at byte `at` of a buffer tensor's storage.
-at::Tensor slice_of(const at::Tensor& buf, at::ScalarType ty, int64_t at, int64_t n) {
+at::Tensor slice_of(const at::Tensor& buf, at::ScalarType ty, int64_t at, at::IntArrayRef sizes) {
   at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buf.storage()), buf.key_set(),
                                                           c10::scalarTypeToTypeMeta(ty));
   t.unsafeGetTensorImpl()->set_storage_offset(at / (int64_t)c10::elementSize(ty));
-  t.unsafeGetTensorImpl()->set_sizes_contiguous(at::IntArrayRef(&n, 1));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
   return t;
 }
 
@@ -218,7 +218,7 @@ PyObject* build_page_maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
             bytes += (sizes[i] * (pass ? 4 : 8) + 15) & ~int64_t(15);
           }
       const at::Tensor buf = at::empty({bytes}, ctx.options().dtype(at::kByte));
-      for (int i = 0; i < 8; ++i) o[i] = slice_of(buf, types[i], at[i], sizes[i]);
+      for (int i = 0; i < 8; ++i) o[i] = slice_of(buf, types[i], at[i], at::IntArrayRef(&sizes[i], 1));
     }
     const qsa_status st = qsa_build_page_maps(
         &d, ctx.data_ptr<int32_t>(), nw.data_ptr<int32_t>(), fp.data_ptr<int32_t>(), bt.data_ptr<int32_t>(),
@@ -664,7 +664,10 @@ PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
     };
     const int32_t *num = ints(a[4], "num_drafts"), *ctx = ints(a[5], "context_lens");
     need(given(a[5]) || !given(a[8]), "next_lens needs context_lens");
-    at::Tensor out[3];
+    at::Tensor out[3], fresh;
+    const int64_t row = (B * 4 + 15) & ~int64_t(15);  // bytes of a [B] output; new ones share an allocation
+    if (!given(a[6]) || !given(a[7]) || (given(a[5]) && !given(a[8])))
+      fresh = at::empty({2 * row + B * (K + 1) * 4}, tok.options().dtype(at::kByte));
     if (given(a[6])) {
       out[0] = tensor(a[6], "tokens");
       need(out[0].dim() == 2 && out[0].scalar_type() == at::kInt && out[0].is_contiguous() && out[0].size(0) == B &&
@@ -672,7 +675,7 @@ PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
            "tokens must be a contiguous int32 [B, K + 1] tensor");
       place.also(out[0]);
     } else {
-      out[0] = at::empty({B, K + 1}, tok.options());
+      out[0] = slice_of(fresh, at::kInt, 2 * row, {B, K + 1});
     }
     for (int i = 1; i < 3; ++i) {
       if (i == 2 && !given(a[5])) break;
@@ -680,7 +683,7 @@ PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
         ints(a[6 + i], i == 1 ? "num_accepted" : "next_lens");
         out[i] = tensor(a[6 + i], "");
       } else {
-        out[i] = at::empty({B}, tok.options());
+        out[i] = slice_of(fresh, at::kInt, (i - 1) * row, {B});
       }
     }
     const qsa_status st =

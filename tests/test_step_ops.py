@@ -444,6 +444,14 @@ def test_windowed_attention(cuda, form, lens, window, sinks, hkv, group, D, pt, 
 
 
 @gpu
+@pytest.mark.parametrize("window,new", [(100, 6), (509, 8), (600, 8), (100, 20)])
+def test_windowed_attention_of_the_dispatch(cuda, window, new):
+    """The form the call chooses itself, on either side of its rule."""
+    windowed(Problem([(1500, new), (90, new), (new, new)], 2, 4, 128, 64, "bf16", seed=new), window, 3, _abi.ATTN_AUTO,
+             max_new=new)
+
+
+@gpu
 @pytest.mark.parametrize("pt", [1, 3, 20, 192])
 def test_windowed_attention_odd_pages(cuda, pt):
     pr = Problem([(333, 2), (41, 5), (7, 7)], 2, 3, 128, pt, "bf16", seed=pt)
