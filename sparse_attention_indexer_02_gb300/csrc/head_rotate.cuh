@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(NORM || LAYOUT == kAny ? 32 * kWarps : 512, 2)
   const int64_t tok0 = (int64_t)blockIdx.x * p.tokens;
   const int tokens = (int)min((int64_t)p.tokens, p.num_tokens - tok0);
 
-  // the lane's chunks: elements e[0] .. e[0] + 7 and e[1] .. e[1] + 7 of its head
+  // the lane's pieces: elements e[c] .. e[c] + kPiece - 1 of its head
   const int sub = lane / LP, i = lane % LP, half = p.rot_dim >> 1;
   // In fours of elements, g = 0..3; a chunk is two of them, but in kHalf4, where a
   // lane has two pairs of fours that are partners.

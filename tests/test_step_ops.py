@@ -960,3 +960,44 @@ print("same")
     res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                          cwd=qbuild.PKG + "/..")
     assert res.returncode == 0 and "same" in res.stdout, res.stderr[-2000:]
+
+
+@gpu
+def test_window_arguments_refused(cuda):
+    pr = Problem([(30, 2)], 2, 4, 128, 16, "bf16", seed=1)
+    with pytest.raises(ValueError, match="selected"):
+        pr.run(window=4, selected=torch.zeros((2, 1), dtype=torch.int32, device="cuda"))
+    for kw in (dict(window=-1), dict(sink_tokens=3), dict(window=3, sink_tokens=-1), dict(window=3, local_tokens=2)):
+        with pytest.raises(qsa.QSAError) as e:
+            pr.run(**kw)
+        assert e.value.status == INVALID
+    for kw in (dict(window=1 << 31), dict(window=2.5), dict(window=3, sink_tokens=None)):
+        with pytest.raises(ValueError):
+            pr.run(**kw)
+    windowed(pr, 2**31 - 1, 0, _abi.ATTN_AUTO)
+
+
+@gpu
+@pytest.mark.parametrize("B,K", [(70, 2), (16, 1), (200, 0)])
+def test_verify_in_every_cluster(cuda, B, K):
+    """Batches that take clusters of every size, over a vocabulary of odd rows too."""
+    for V in (140000, 9001):
+        tokens, target, u, draft = _drafted(B, K, V, torch.bfloat16 if V > 100000 else torch.float32, B)
+        got = torch_api.verify_drafts(tokens, target, u, draft_probs=draft)
+        acc = got.num_accepted.long()
+        at = torch.arange(B, device="cuda")
+        # against integers on the GPU: the row's weights in units, their cumulative sums, the point
+        unit = lambda x: torch.round(x.double().clamp(0, 1) * 2.0 ** 45).long()  # noqa: E731
+        w = unit(target[at, acc])
+        if K:
+            left = (w - unit(draft[at, acc.clamp(max=K - 1)])).clamp(min=0)
+            some = (acc < K) & (left.sum(1) > 0)
+            w = torch.where(some[:, None], left, w)
+        cum = w.cumsum(1)
+        total = cum[:, -1]
+        m = (u[:, K].double() * 2.0 ** 24).long()          # u is a multiple of 2^-24
+        # cum > u total  <=>  cum 2^24 > m total, with total = hi 2^24 + lo
+        hi, lo = total >> 24, total & ((1 << 24) - 1)
+        point = m * hi + ((m * lo) >> 24)
+        want = (cum <= point[:, None]).sum(1)
+        assert torch.equal(got.tokens[at, acc].long(), want)
