@@ -409,10 +409,12 @@ __global__ void __launch_bounds__(kNT, 1)
                       &empty[stage], st == nst - 1);
         // After the item's last scores q's place is free: the next item's q, and its first keys
         // and values behind it, are on their way during the last softmax and product (1024 items
-        // of one key tile 58 -> 46 us, 8 x 1000 new tokens 102 -> 94, 8192 at 8192 396 -> 376;
-        // items of 33 tiles as before, to 2 %).
+        // of one key tile 58 -> 45 us, 8 x 1000 new tokens 100 -> 93; the 8 K chunk at 32 K 2105 ->
+        // 2053, 2137 with the release looked for beside the scores of each stream).
         if (ua + 1 >= uz) ptx::mma_commit_elect(&q_bar[1]);
         advance();
+        const int release = uz - 2;
+#pragma unroll 1
         for (int j = ua; j < uz; ++j) {
           const uint32_t vst = stage;
           ok = wwait(&full[vst], phase);
@@ -474,11 +476,13 @@ __global__ void __launch_bounds__(kNT, 1)
               }
               issue_qk<D>(tmem + st * 128, q_lo + st * kTile16, k_lo + stage * kTile16, qk_hi, id_qk, &s_full[st],
                           &empty[stage], last);
-              if (last && j + 2 >= uz) ptx::mma_commit_elect(&q_bar[1]);
             }
           }
           if (!ok) break;
-          if (more) advance();
+          if (more) {
+            advance();
+            if (__builtin_expect(j == release, 0)) ptx::mma_commit_elect(&q_bar[1]);
+          }
         }
         if (!ok || last_item) break;
       }
