@@ -687,7 +687,8 @@ typedef struct qsa_head_rows {
  * part, with a = positions[t] * f_i:
  *   lo' = m (lo cos a - hi sin a),   hi' = m (hi cos a + lo sin a);
  * elements beside the rotated part stay n (without a norm: their bits).  All in
- * fp32, rounded to the rows' type once.  Rows with a negative position are
+ * fp32, rounded to the rows' type once (with a norm a head's squares add up below
+ * 2^127).  Rows with a negative position are
  * padding: their outputs are not written.
  *
  * freqs: device uint64 [R / 2], f_i / (2 pi) in units of 2^-64, modulo 2^64: the

@@ -154,7 +154,8 @@ def windowed(pool: PagedPool, block_table: torch.Tensor, maps: torch_api.PageMap
     torch_api.build_page_maps): the tokens' keys and values are stored in `pool`,
     rotated first if asked, and every token attends to its last `window` tokens,
     itself among them, and to the first sink_tokens ones.  Any number of tokens a
-    request; max_new as in torch_api.paged_attention."""
+    request; max_new as in torch_api.paged_attention.  The pool's pages hold as
+    many tokens as the maps were built for, and their ids are the maps'."""
     q = _store(pool, maps, q, k, v, rotation)
     return WindowResult(*torch_api.paged_attention(q, pool.k_cache, pool.v_cache, block_table, maps.query_start,
                                                    maps.seq_lens, scale=scale, max_new=max_new, window=window,
