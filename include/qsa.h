@@ -747,8 +747,10 @@ typedef struct qsa_verify_desc {
  * Probabilities are clamped to [0, 1] (NaN: 0), those of a row add up to 1024 at
  * most (else the request's outputs are unspecified).  Weights count in units
  * of 2^-45, so sums are exact and the result does not depend on their order.
- * u outside [0, 1) is taken as the nearest inside (NaN: 0).  No weight at all:
- * the next token is -1.  Rows past n (target) and n - 1 (draft) may hold
+ * u lies in [0, 1); below it and NaN count as 0.  From 1 on, u[i] counts as 1
+ * (the formula then refuses a draft with q = p, which every u below 1 accepts:
+ * numbers from (0, 1] are given as 1 - u) and u[K] as 1 - 2^-64.  No weight at
+ * all: the next token is -1.  Rows past n (target) and n - 1 (draft) may hold
  * anything; so may draft_tokens past n.
  *
  * Device pointers: target_probs [B][K + 1][V] and draft_probs [B][K][V] of the

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kNT, 2) verify_kernel(const VerifyParams p, in
       if (x >= 0 && x < p.vocab) {
         const double pt = prob_at(target + (int64_t)i * p.target_row, x);
         const double qd = draft ? prob_at(draft + (int64_t)i * p.draft_row, x) : 1.0;
-        ok = (double)u[i] * qd < pt;
+        ok = (double)__saturatef(u[i]) * qd < pt;  // (saturated, NaN is 0)
       }
     }
     const uint32_t refused = __ballot_sync(kAll, i < n && !ok);

@@ -386,11 +386,12 @@ def verify_drafts(draft_tokens: torch.Tensor, target_probs: torch.Tensor, unifor
 
     draft_tokens: int32 [B, K] (K 0: the next token alone is drawn); target_probs:
     fp32, bf16 or fp16 [B, K + 1, V], rows contiguous; uniforms: fp32 [B, K + 1] in
-    [0, 1): one a draft, the last for the next token; draft_probs: [B, K, V] in
-    the same type (None: certain drafts, accepted with the target's probability);
-    num_drafts: int32 [B] drafts a request brings (None: K).  With context_lens,
-    int32 [B] tokens in the cache before the step, next_lens are the ones that
-    count after it (the rejected drafts' slots are overwritten by later steps)."""
+    [0, 1): one a draft, the last for the next token (from a generator over (0, 1],
+    give 1 - u); draft_probs: [B, K, V] in the same type (None: certain drafts,
+    accepted with the target's probability); num_drafts: int32 [B] drafts a request
+    brings (None: K).  With context_lens, int32 [B] tokens in the cache before the
+    step, next_lens are the ones that count after it (the rejected drafts' slots are
+    overwritten by later steps)."""
     if stream is not None:
         with _on(stream):
             return verify_drafts(draft_tokens, target_probs, uniforms, draft_probs=draft_probs, num_drafts=num_drafts,
