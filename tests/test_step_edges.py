@@ -1,13 +1,15 @@
 """Edges of the step operators: calls that the documentation allows and a plain
 step does not make (the operators themselves: test_step_ops.py)."""
 import math
+from fractions import Fraction
 
 import pytest
 
 torch = pytest.importorskip("torch")
 
-from sparse_attention_indexer_02_gb300 import torch_api  # noqa: E402
-from test_step_ops import cuda, gpu, lib  # noqa: E402,F401
+from sparse_attention_indexer_02_gb300 import _abi, torch_api  # noqa: E402
+from test_serving_ops import Problem, _cu  # noqa: E402
+from test_step_ops import _drafted, cuda, gpu, lib  # noqa: E402,F401
 
 
 # ---------------------------------------------------------------------------
@@ -46,3 +48,89 @@ def test_verify_acceptance_numbers_past_their_ends(cuda, dt, V, certain):
     assert got.num_accepted.tolist() == want
     # refused: the first token with weight left; u[1] = 0 draws it (token 2, it has 0.5 of p alone)
     assert got.tokens.tolist() == [[x, 7] if a else [2, -1] for a in want]
+
+
+@gpu
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("B,K", [(70, 2), (16, 1), (16, 40), (200, 3)])
+@pytest.mark.parametrize("V", [140000, 9001])
+@pytest.mark.parametrize("certain", [False, True])
+def test_verify_whole_rows_in_every_cluster(cuda, dt, B, K, V, certain):
+    """Accepted counts by comparisons of their own, and every entry of the outputs."""
+    if B * K * V > 200 * 2 * 140000:
+        B = max(1, 200 * 2 * 140000 // (K * V))
+    tokens, target, u, draft = _drafted(B, K, V, dt, B + K, spread=1.0)
+    g = torch.Generator(device="cuda").manual_seed(V)
+    num = torch.randint(-1, K + 2, (B,), generator=g, dtype=torch.int32, device="cuda")
+    ctx = torch.randint(0, 9000, (B,), generator=g, dtype=torch.int32, device="cuda")
+    got = torch_api.verify_drafts(tokens, target, u, draft_probs=None if certain else draft, num_drafts=num,
+                                  context_lens=ctx)
+    at = tokens.long()[..., None]
+    p = target[:, :K].gather(2, at)[..., 0].double()
+    q = torch.ones_like(p) if certain else draft.gather(2, at)[..., 0].double()
+    n = num.clamp(0, K)
+    refused = ~(u[:, :K].double() * q < p) & (torch.arange(K, device="cuda") < n[:, None])
+    acc = torch.where(refused.any(1), refused.int().argmax(1), n).long()
+    assert torch.equal(got.num_accepted.long(), acc)
+    assert torch.equal(got.next_lens, (ctx + 1 + acc).int())
+    # the token after them, in whole units of 2^-45 (no sum passes 2^46)
+    i = torch.arange(B, device="cuda")
+    unit = lambda x: torch.round(x.double() * 2.0 ** 45).long()  # noqa: E731
+    w, k = unit(target[i, acc]), acc.clamp(max=K - 1)
+    if certain:
+        left = w.scatter(1, tokens[i, k].long()[:, None], 0)
+    else:
+        left = (w - unit(draft[i, k])).clamp(min=0)
+    w = torch.where(((acc < n) & (left.sum(1) > 0))[:, None], left, w)
+    # floor(u total) in Python integers (u is no multiple of 2^-24 where it is small)
+    point = [math.floor(Fraction(x) * t) for x, t in zip(u[:, K].tolist(), w.sum(1).tolist())]
+    point = torch.tensor(point, device="cuda")
+    nxt = (w.cumsum(1) <= point[:, None]).sum(1)
+    want = torch.full((B, K + 1), -1, device="cuda")
+    j = torch.arange(K, device="cuda")
+    want[:, :K] = torch.where(j < acc[:, None], tokens.long(), -1)
+    want[i, acc] = nxt
+    assert torch.equal(got.tokens.long(), want)
+
+
+# ---------------------------------------------------------------------------
+# windows
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("form", [_abi.ATTN_GATHER, _abi.ATTN_TILE], ids=["gather", "tile"])
+@pytest.mark.parametrize("sinks", [0, 20, 33])
+@pytest.mark.parametrize("past", [1, 20, 50, 75])
+def test_windows_across_the_tables_end(cuda, form, sinks, past):
+    """Rows whose windows begin before the last page's end and end behind it: the
+    keys from the window's start to the end of the table, and the sinks."""
+    pr = Problem([(384, 40), (64, 3)], 2, 4, 128, 32, "bf16", seed=21)
+    cap = 384
+    table = pr.table[:, :cap // 32].contiguous()
+    out, lse = torch_api.paged_attention(pr.q, pr.kc, pr.vc, table, pr.start, _cu([cap + past, 64]), scale=pr.scale,
+                                         return_lse=True, form=form, window=60, sink_tokens=sinks)
+    rows = [[t for t in range(min(p + 1, cap)) if t < sinks or t > p - 60] for p in range(cap + past - 40, cap + past)]
+    rows += [[t for t in range(p + 1) if t < sinks or t > p - 60] for p in range(61, 64)]
+    T, H, D = pr.q.shape
+    u = 2.0 ** -8
+    for b, (first, n) in enumerate(((0, 40), (40, 3))):
+        tok = torch.arange(cap if b == 0 else 64, device="cuda")
+        at = table[b].long()[tok // 32] * 32 + tok % 32
+        k, v = (c.flatten(0, 1)[at].double() for c in (pr.kc, pr.vc))
+        see = torch.zeros((n, len(tok)), dtype=torch.bool, device="cuda")
+        for i in range(n):
+            see[i, rows[first + i]] = True
+        for h in range(H):
+            q = pr.q[first:first + n, h].double()
+            x = torch.where(see, q @ k[:, h // 4].T * pr.scale, -math.inf)
+            z = torch.logsumexp(x, 1)
+            p = torch.where(see, torch.exp(x - z.clamp(min=-1e300)[:, None]), 0.0)
+            o, mag = p @ v[:, h // 4], p @ v[:, h // 4].abs()
+            # half a step of the output and of every probability; scores: D products and sums in fp32
+            dx = (D + 2) * 2.0 ** -23 * torch.where(see, q.abs() @ k[:, h // 4].abs().T, 0.0).amax(1) * pr.scale
+            slack = 2 * dx + see.sum(1) * 2.0 ** -24 + 2.0 ** -20
+            got, gl = out[first:first + n, h].double(), lse[first:first + n, h].double()
+            assert ((got - o).abs() <= u * (o.abs() + mag) + mag * slack[:, None]).all(), (b, h)
+            empty = see.sum(1) == 0
+            assert (got[empty] == 0).all() and (gl[empty] == -math.inf).all()
+            assert ((gl - z).abs()[~empty] <= (slack + 2.0 ** -22 * z.abs())[~empty]).all(), (b, h)
