@@ -12,13 +12,19 @@ verified after its last layer:
     win = windowed(other_pool, block_table, res.maps, q=q, k=k, v=v, window=4096, sink_tokens=4,
                    rotation=HeadRotation(rotary, norm="rms", q_weight=wq, k_weight=wk))
     ver = torch_api.verify_drafts(drafts, target_probs, uniforms, draft_probs=dp, context_lens=context_lens)
+
+The next maps put a new page into every entry of the table from the next lengths
+on, also where a page of refused tokens alone is still listed.  Such pages go back
+to the free list before that (their ids are lost with the entries):
+
+    j = torch.arange(block_table.shape[1], device=block_table.device)
+    kept, held = (-(-n[:, None] // pool.page_tokens) for n in (ver.next_lens, res.maps.seq_lens))
+    refused = block_table[(j >= kept) & (j < held) & (block_table >= 0)]
+    free_pages = torch.cat([free_pages[int(res.maps.pages_used):], refused])
     context_lens = ver.next_lens
 
-(The pages of table entries past the next lengths hold refused tokens only; the
-caller may return them to its free list, or leave them: the next maps overwrite
-the entries.)
-
-Every call goes to the current stream, nothing waits for the device, and the
+(This reads how many pages there are, so it waits for the device.)  Every call
+itself goes to the current stream, nothing in it waits for the device, and the
 shapes depend on host values only, so a step can be captured in a CUDA graph.
 """
 from __future__ import annotations

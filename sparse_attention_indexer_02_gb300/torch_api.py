@@ -390,8 +390,9 @@ def verify_drafts(draft_tokens: torch.Tensor, target_probs: torch.Tensor, unifor
     give 1 - u); draft_probs: [B, K, V] in the same type (None: certain drafts,
     accepted with the target's probability); num_drafts: int32 [B] drafts a request
     brings (None: K).  With context_lens, int32 [B] tokens in the cache before the
-    step, next_lens are the ones that count after it (the rejected drafts' slots are
-    overwritten by later steps)."""
+    step, next_lens are the ones that count after it (later steps overwrite the
+    rejected drafts' slots in the pages that next_lens keep; the pages past them are
+    the caller's to free before the next page maps, as in serving's text)."""
     if stream is not None:
         with _on(stream):
             return verify_drafts(draft_tokens, target_probs, uniforms, draft_probs=draft_probs, num_drafts=num_drafts,

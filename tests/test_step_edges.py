@@ -1,13 +1,16 @@
 """Edges of the step operators: calls that the documentation allows and a plain
 step does not make (the operators themselves: test_step_ops.py)."""
 import math
+import re
+import textwrap
+import types
 from fractions import Fraction
 
 import pytest
 
 torch = pytest.importorskip("torch")
 
-from sparse_attention_indexer_02_gb300 import _abi, torch_api  # noqa: E402
+from sparse_attention_indexer_02_gb300 import _abi, serving, torch_api  # noqa: E402
 from test_serving_ops import Problem, _cu  # noqa: E402
 from test_step_ops import _drafted, cuda, gpu, lib  # noqa: E402,F401
 
@@ -134,3 +137,44 @@ def test_windows_across_the_tables_end(cuda, form, sinks, past):
             empty = see.sum(1) == 0
             assert (got[empty] == 0).all() and (gl[empty] == -math.inf).all()
             assert ((gl - z).abs()[~empty] <= (slack + 2.0 ** -22 * z.abs())[~empty]).all(), (b, h)
+
+
+# ---------------------------------------------------------------------------
+# rounds of drafts
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("K", [1, 3, 20])
+def test_documented_rounds_lose_no_page(cuda, K):
+    """The lines of serving's text between a verification and the next step, in a
+    pool that suffices only if the pages of refused tokens come back."""
+    lines = re.search(r"\n\n((?:    [^\n]*\n)*    context_lens = ver\.next_lens\n)", serving.__doc__).group(1)
+    B, P, rounds, V = 5, 4, 40, 64
+    start = [3, 4, 1, 9, 16]
+    # every request's tokens after the last round (three in two rounds), and a round's drafts
+    pages = sum(-(-(n + rounds * 3 // 2 + K + 1) // P) for n in start)
+    pool = serving.PagedPool(num_pages=pages, page_tokens=P, num_kv_heads=1, head_dim=64)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    free_pages = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    block_table = torch.full((B, pages), -1, dtype=torch.int32, device="cuda")
+    maps = torch_api.build_page_maps(_cu([0] * B), _cu(start), free_pages, block_table, page_tokens=P, max_tokens=sum(start))
+    free_pages = free_pages[int(maps.pages_used):]
+    context_lens, total = _cu(start), list(start)
+    for turn in range(rounds):
+        maps = torch_api.build_page_maps(context_lens, _cu([K + 1] * B), free_pages, block_table, page_tokens=P,
+                                         max_tokens=B * (K + 1))
+        assert int(maps.pages_used) <= len(free_pages) and (maps.slots >= 0).all()
+        # certain drafts: the first is the target's own in every other round, the second never is
+        target = torch.zeros((B, K + 1, V), device="cuda")
+        target[:, :, 7] = 1.0
+        drafts = torch.full((B, K), 8, dtype=torch.int32, device="cuda")
+        drafts[:, 0] = 7 + turn % 2
+        ver = torch_api.verify_drafts(drafts, target, torch.full((B, K + 1), 0.5, device="cuda"), context_lens=context_lens)
+        names = dict(torch=torch, ver=ver, res=types.SimpleNamespace(maps=maps), pool=pool, block_table=block_table,
+                     free_pages=free_pages, context_lens=context_lens)
+        exec(textwrap.dedent(lines), names)
+        free_pages, context_lens = names["free_pages"], names["context_lens"]
+        total = [n + 2 - turn % 2 for n in total]
+        assert context_lens.tolist() == total
+        live = [block_table[b, :-(-n // P)] for b, n in enumerate(total)]
+        assert sorted(torch.cat(live + [free_pages]).tolist()) == list(range(pages))
