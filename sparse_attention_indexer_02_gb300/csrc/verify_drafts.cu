@@ -159,7 +159,7 @@ struct Rows {
   // Piece n holds the tokens first(n) .. first(n) + kV - 1.
   __device__ __forceinline__ int32_t first(int32_t n) const { return n * kV - off; }
   __device__ __forceinline__ uint4 one_by_one(const T* row, int32_t j) const {
-    T e[kV];
+    alignas(16) T e[kV];
 #pragma unroll
     for (int i = 0; i < kV; ++i) e[i] = j + i >= 0 && j + i < vocab ? row[j + i] : T(0.0f);
     return *reinterpret_cast<const uint4*>(e);
