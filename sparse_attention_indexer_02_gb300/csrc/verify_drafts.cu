@@ -314,6 +314,7 @@ __global__ void __launch_bounds__(kNT, 2) verify_kernel(const VerifyParams p, in
                    : "r"(ptx::smem_u32(&cta_sum[attempt][rank])), "r"((int)threadIdx.x));
       asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote), "l"(mine) : "memory");
     }
+    __syncwarp();  // the barrier takes whole warps
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
     all = 0;
     for (int c = 0; c < cluster; ++c) all += cta_sum[attempt][c];
