@@ -82,6 +82,8 @@ class Rotary:
             raise ValueError("rot_dim must be even, with rot_dim / 2 frequencies")
         if not all(math.isfinite(f) for f in frequencies) or not math.isfinite(magnitude):
             raise ValueError("frequencies and magnitude must be finite")
+        if offset != int(offset):
+            raise ValueError("offset must be a whole number")
         self.rot_dim, self.layout, self.offset, self.magnitude = rot_dim, _LAYOUTS[layout], int(offset), float(magnitude)
         self.frequencies = frequencies
         turns = [int(round(math.ldexp(math.fmod(f / (2 * math.pi), 1.0), 64))) % (1 << 64) for f in frequencies]

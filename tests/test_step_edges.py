@@ -10,9 +10,22 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from sparse_attention_indexer_02_gb300 import _abi, serving, torch_api  # noqa: E402
+from sparse_attention_indexer_02_gb300 import _abi, rotary, serving, torch_api  # noqa: E402
 from test_serving_ops import Problem, _cu  # noqa: E402
 from test_step_ops import _drafted, cuda, gpu, lib  # noqa: E402,F401
+
+
+# ---------------------------------------------------------------------------
+# rotation
+# ---------------------------------------------------------------------------
+
+def test_rotary_offsets_are_whole_numbers():
+    """A fraction is refused, not cut off."""
+    for offset in (1.5, 63.999, -0.5):
+        with pytest.raises(ValueError, match="offset"):
+            rotary.Rotary(64, offset=offset, device="cpu")
+    for offset in (2, 2.0):
+        assert rotary.Rotary(64, offset=offset, device="cpu").offset == 2
 
 
 # ---------------------------------------------------------------------------
