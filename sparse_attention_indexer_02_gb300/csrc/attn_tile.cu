@@ -12,11 +12,14 @@
 //   O = O + P V (128 x D, fp32 in TMEM; P as 16-bit in TMEM over S, V from
 //                shared memory, where its rows are keys: the MN-major operand)
 //
+// P is rounded to the type the second product takes, by at most 2^-8 or 2^-11 of a
+// term; l is the sum of the fp32 values.
+//
 // TMEM is full: S/P and O of both streams are 2 * 128 + 2 * D columns.
 // What bounds a chunk is the tensor core (4 * D flop a row and key): 8192 new
-// tokens at 32768, 32 heads of 128, take 2090 to 2170 us alone, 1775 to 1840
-// TFLOP/s, 0.93 to 0.97 of the measured bf16 rate, and 2550 to 2660 back to back,
-// 1450 to 1510 TFLOP/s, under the power limit (a library product keeps 1733
+// tokens at 32768, 32 heads of 128, take 2050 to 2120 us alone, 1815 to 1880
+// TFLOP/s, 0.95 to 0.99 of the measured bf16 rate, and 2360 to 2520 back to back,
+// 1530 to 1630 TFLOP/s, under the power limit (a library product keeps 1733
 // there).  The exponentials are half its time.  The two streams exist to keep it busy: the
 // softmax of one runs while the MMAs of the other do.  Two tiles on one key
 // tile also halve what L2 has to deliver, 64 KB for 2048 cycles of MMA.

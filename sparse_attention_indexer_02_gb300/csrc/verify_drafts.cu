@@ -19,7 +19,7 @@
 // few requests the chain of loads ahead of the row (the drafts, their
 // probabilities), the row, and the cluster's exchange; between the two the sums'
 // instructions.  Units comes to six a value: integer significands shifted into 64
-// bits took 54 (those instructions run at half rate or less), 27 us for 64 requests
+// bits took 54 (those instructions run at half rate or less), 32 us for 64 requests
 // x 131072 tokens, three exact fp32 accumulators nine, 20 us.
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>

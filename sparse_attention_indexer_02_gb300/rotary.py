@@ -10,7 +10,8 @@ rotated elements, changed for contexts longer than a model was trained on:
   parts    pairs that turn often over the original context stay, those that do
            not complete a turn are divided by factor, a ramp between: with
            r_i = original f_i / (2 pi) turns and g = clamp((r_i - low) / (high - low), 0, 1),
-           f_i (g + (1 - g) / factor)
+           f_i (g + (1 - g) / factor).  The ramp runs over the turns; a model whose ramp
+           runs over the pairs' indexes i has other values between: give its `frequencies`
 
 `magnitude` multiplies the cosines and sines (an attention temperature that some
 scalings bring along, such as 0.1 ln(factor) + 1).
